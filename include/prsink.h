@@ -21,7 +21,8 @@
  *     device status word; prsink_sync_status() reads and clears it.  There is ONE status word
  *     per device, shared by every stream and host thread that uses the library on it: a
  *     timeout raised by a kernel on stream A is reported (and cleared) by a
- *     prsink_sync_status() call made for stream B.
+ *     prsink_sync_status() call made for stream B.  The paged calls record lengths and page
+ *     indices they had to refuse on the device in the same word (PRSINK_ERR_PAGE).
  *
  * Cache layout (the "slot-indexed" cache).  For one layer, K and V caches are each
  * bf16 [H][T][d] (head-major, d contiguous).  Physical key rows are grouped in slots:
@@ -50,6 +51,8 @@ extern "C" {
 #define PRSINK_ERR_LAUNCH      (-3)  /* CUDA error; text from prsink_last_error()          */
 #define PRSINK_ERR_TIMEOUT     (-4)  /* a bounded device wait ran out (see sync_status)    */
 #define PRSINK_ERR_UNSUPPORTED (-5)  /* valid but not supported here (e.g. head_dim 96)    */
+#define PRSINK_ERR_PAGE        (-6)  /* a device-side length or page index was out of range
+                                        (paged calls; see sync_status)                      */
 
 #define PRSINK_SLOT_REF     0
 #define PRSINK_SLOT_STATIC  1
@@ -344,9 +347,118 @@ int prsink_bank_update_policy(const prsink_layout* layout, const prsink_bank_pol
                               const float* phi_b, long long b, int* action_out, int* mode_out,
                               const void* cache_kv, void* bank_kv, int n_layers, void* stream);
 
+/* Gradient of prsink_attention with respect to its raw queries, raw keys and values.
+ *
+ * For each head, with q~, k~ the rotated queries and keys, s = q~ k~^T / sqrt(d) over the valid
+ * keys and the forward's lse: the probabilities are recomputed, P = exp(s - lse), and
+ *   delta_i = sum_c d_out_ic out_ic,  dP = d_out V^T,  dS = P o (dP - delta) / sqrt(d),
+ *   dV = P^T d_out,  dK = R^T (dS^T q~),  dQ = R^T (dS k~)
+ * (R^T: the rotation of the row's position, inverted, so that the gradients are those of the raw
+ * vectors the cache holds).  No atomics: the same inputs give the same bits.
+ *
+ *   q, k_cache, v_cache, dyn_src   as given to the forward call
+ *   out        bf16 [L_blk][H][d]  the forward's output
+ *   lse        f32  [H][L_blk]     the forward's lse (required)
+ *   d_out      bf16 [L_blk][H][d]  gradient of the output
+ *   dq         bf16 [L_blk][H][d]  written
+ *   dk, dv     bf16 [H][T][d]      the rows of the slots in `grad_mask` are written, no other
+ *              byte; rows of slots without data (valid_mask, dyn_src) get zeros.  Both may be
+ *              NULL when grad_mask selects no slot (gradient of the queries alone).
+ *   grad_mask  bit i = slot i's keys and values need their gradient (~0u: all).  A replay that
+ *              holds the history fixed passes the bit of the current block's ring slot only.
+ *   scratch    device memory of prsink_attention_backward_scratch_bytes(layout) bytes, 256-byte
+ *              aligned, owned by the caller, not shared with a concurrent call
+ * Rows whose lse is -inf (no valid key) contribute nothing and get dq = 0.  P and dS are rounded
+ * to bf16 as tensor-core operands, as are the rotated q and k; statistics and sums are f32.
+ * Errors: PRSINK_ERR_ARG, PRSINK_ERR_ALIGN, PRSINK_ERR_UNSUPPORTED, PRSINK_ERR_LAUNCH. */
+int prsink_attention_backward(const prsink_layout* layout, const void* q, const void* k_cache,
+                              const void* v_cache, const void* out, const float* lse,
+                              const void* d_out, void* dq, void* dk, void* dv,
+                              unsigned grad_mask, const long long* dyn_src, void* scratch,
+                              long long scratch_bytes, void* stream);
+
+/* Scratch bytes prsink_attention_backward needs for `layout` (-1 for an invalid layout). */
+long long prsink_attention_backward_scratch_bytes(const prsink_layout* layout);
+
+/* ---- paged cache ----------------------------------------------------------------------
+ * A cache shared by many sequences, in pages of page_size tokens:
+ *   k_pages, v_pages  bf16 [n_pages][n_kv_heads][page_size][d]  (head-major inside a page)
+ *   page_table        int32 [n_seqs][max_pages]   page of tokens [p*page_size, (p+1)*page_size)
+ *   seq_lens          int32 [n_seqs]              tokens of each sequence
+ * The slot-indexed cache above belongs to one stream and holds raw keys whose positions change
+ * from block to block; here a token keeps its index in its sequence for good, so its key is
+ * rotated once, when it is appended.  Tables and lengths stay on the device (a captured graph
+ * can be replayed while they change).  Pages may be shared by sequences (read only).
+ *
+ * Lengths and page indices are checked on the device: a length is clamped to
+ * [0, max_pages*page_size], a page index outside [0, n_pages) that a call has to use makes that
+ * page's tokens absent (not written, not attended), and PRSINK_ERR_PAGE is recorded for
+ * prsink_sync_status().  No access leaves the buffers. */
+typedef struct prsink_paged {
+  int n_seqs;            /* rows of page_table; 0 = nothing to do                           */
+  int n_heads;           /* query heads, a multiple of n_kv_heads                           */
+  int n_kv_heads;        /* key/value heads; query head h reads key head h / (n_heads/n_kv_heads) */
+  int head_dim;          /* d, 64 or 128                                                    */
+  int page_size;         /* tokens of a page: a multiple of 8 up to 128, or any size above  */
+  int n_pages;           /* pages of the pool                                               */
+  int max_pages;         /* columns of page_table                                           */
+  int rope_mode;         /* 0 = no rotation; 1 = 1-D over the token index; 3 = 3-D (t,h,w)  */
+  int rope_split[3];     /* as prsink_layout (3-D mode)                                     */
+  float rope_base;       /* as prsink_layout                                                */
+  int grid_h, grid_w;    /* 3-D mode: token i sits at frame i / (grid_h*grid_w), row, column */
+  int n_sink;            /* attention: first tokens of a sequence that stay attended, and    */
+  int window;            /* the last tokens attended (0 = every token)                      */
+} prsink_paged;
+
+/* Append K and V of new tokens, the rotation of their positions applied on the way.
+ *
+ * The new tokens of all sequences are packed in order; those of sequence s are the rows
+ * [cu_new[s], cu_new[s+1]) and become the LAST tokens of the sequence: row cu_new[s] + i is token
+ * seq_lens[s] - (cu_new[s+1] - cu_new[s]) + i (seq_lens already counts them).
+ *   k_new, v_new  bf16 [n_tokens][n_kv_heads][d], rows k_stride / v_stride elements apart
+ *   q, q_rot      optional (both or neither): bf16 [n_tokens][n_heads][d] queries of the same
+ *                 tokens (rows q_stride apart), written rotated to q_rot (contiguous; may be q
+ *                 itself when q is contiguous)
+ *   cu_new        int32 [n_seqs + 1] on the device, or NULL: one token per sequence
+ *                 (n_tokens = n_seqs); a sequence of length 0 is then an idle row, left alone
+ * Rows from cu_new[n_seqs] on are ignored, their q_rot left as it was.  V is copied bit for bit,
+ * K and q are rotated in f32 by angles reduced in f64 and rounded once (copied when rope_mode is
+ * 0).  No other byte of the pages is written.  Strides are multiples of 8.
+ * Errors: PRSINK_ERR_ARG, PRSINK_ERR_ALIGN, PRSINK_ERR_UNSUPPORTED, PRSINK_ERR_LAUNCH; on the
+ * device PRSINK_ERR_PAGE (a token with no page or outside [0, max_pages*page_size)). */
+int prsink_paged_append(const prsink_paged* paged, const void* k_new, const void* v_new,
+                        long long k_stride, long long v_stride, void* k_pages, void* v_pages,
+                        const int* page_table, const int* seq_lens, int n_tokens,
+                        const int* cu_new, const void* q, long long q_stride, void* q_rot,
+                        void* stream);
+
+/* Attention of one new token per sequence over the paged cache, the bound of the PR-Sink cache
+ * (sinks and a rolling window) given in tokens.
+ *
+ * out = softmax(q k^T / sqrt(d)) v over the tokens i < seq_lens[s] with i < n_sink or
+ * i >= seq_lens[s] - window (every token when window = 0).  Pages without such a token are not
+ * read and their table entries not looked at (evicted pages may hold any index).
+ * The work is divided evenly over the SMs along the tokens of all sequences and heads; where a
+ * (sequence, head) is shared by several CTAs, the last one to finish joins their partial results
+ * in a fixed order (the same inputs give the same bits on the same device).
+ *   q        bf16 [n_seqs][n_heads][d]   rotated queries (prsink_paged_append)
+ *   out      bf16 [n_seqs][n_heads][d]   written; 0 for a sequence with nothing to attend
+ *   lse      f32  [n_seqs][n_heads]      natural log-sum-exp (-inf likewise), or NULL
+ *   scratch  device memory of prsink_paged_attention_scratch_bytes(paged) bytes, 256-byte
+ *            aligned, owned by the caller, not shared with a concurrent call
+ * Errors: as prsink_paged_append. */
+int prsink_paged_attention(const prsink_paged* paged, const void* q, const void* k_pages,
+                           const void* v_pages, const int* page_table, const int* seq_lens,
+                           void* out, float* lse, void* scratch, long long scratch_bytes,
+                           void* stream);
+
+/* Scratch bytes prsink_paged_attention needs on the current device (-1 for an invalid argument). */
+long long prsink_paged_attention_scratch_bytes(const prsink_paged* paged);
+
 /* Synchronise `stream`, then read and clear the status word of the current device:
  * PRSINK_OK, or PRSINK_ERR_TIMEOUT if a bounded wait of any kernel on this device (any
- * stream) ran out since the word was last cleared, or PRSINK_ERR_LAUNCH.  Only `stream` is
+ * stream) ran out since the word was last cleared, or PRSINK_ERR_PAGE if a paged call met a
+ * length or page index out of range (a timeout is reported first), or PRSINK_ERR_LAUNCH.  Only `stream` is
  * synchronised: kernels still running on other streams may report later. */
 int prsink_sync_status(void* stream);
 

@@ -9,3 +9,4 @@ the sources are silent.
 """
 from .prsink_oracle import *  # noqa: F401,F403
 from .prsink_oracle import __all__  # noqa: F401
+from .paged import *  # noqa: F401,F403,E402

@@ -23,6 +23,7 @@ PRSINK_ERR_ALIGN = -2
 PRSINK_ERR_LAUNCH = -3
 PRSINK_ERR_TIMEOUT = -4
 PRSINK_ERR_UNSUPPORTED = -5
+PRSINK_ERR_PAGE = -6
 
 SLOT_REF, SLOT_STATIC, SLOT_DYNAMIC, SLOT_RING0 = 0, 1, 2, 3
 FP_DIM = 558
@@ -31,7 +32,7 @@ MAX_RING = 8
 
 _NAMES = {PRSINK_ERR_ARG: "PRSINK_ERR_ARG", PRSINK_ERR_ALIGN: "PRSINK_ERR_ALIGN",
           PRSINK_ERR_LAUNCH: "PRSINK_ERR_LAUNCH", PRSINK_ERR_TIMEOUT: "PRSINK_ERR_TIMEOUT",
-          PRSINK_ERR_UNSUPPORTED: "PRSINK_ERR_UNSUPPORTED"}
+          PRSINK_ERR_UNSUPPORTED: "PRSINK_ERR_UNSUPPORTED", PRSINK_ERR_PAGE: "PRSINK_ERR_PAGE"}
 
 
 class PRSinkError(RuntimeError):
@@ -48,6 +49,17 @@ class Layout(ctypes.Structure):
                 ("ring_slots", ctypes.c_int), ("rope_mode", ctypes.c_int),
                 ("rope_split", ctypes.c_int * 3), ("rope_base", ctypes.c_float),
                 ("block_index", ctypes.c_longlong), ("valid_mask", ctypes.c_uint)]
+
+
+class Paged(ctypes.Structure):
+    """Mirror of ``prsink_paged``."""
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_heads", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("rope_mode", ctypes.c_int),
+                ("rope_split", ctypes.c_int * 3), ("rope_base", ctypes.c_float),
+                ("grid_h", ctypes.c_int), ("grid_w", ctypes.c_int),
+                ("n_sink", ctypes.c_int), ("window", ctypes.c_int)]
 
 
 BANK_FROZEN, BANK_DECAY, BANK_GATED = 0, 1, 2
@@ -85,13 +97,28 @@ def make_layout(n_heads, head_dim, grid_h, grid_w, frames_per_block=3, ref_frame
     return lay
 
 
+def make_paged(n_seqs, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages,
+               rope_mode=1, rope_split=(0, 0, 0), rope_base=10000.0, grid_h=1, grid_w=1,
+               n_sink=0, window=0) -> Paged:
+    pg = Paged()
+    pg.n_seqs, pg.n_heads, pg.n_kv_heads = int(n_seqs), int(n_heads), int(n_kv_heads)
+    pg.head_dim, pg.page_size = int(head_dim), int(page_size)
+    pg.n_pages, pg.max_pages = int(n_pages), int(max_pages)
+    pg.rope_mode, pg.rope_base = int(rope_mode), float(rope_base)
+    for i in range(3):
+        pg.rope_split[i] = int(rope_split[i])
+    pg.grid_h, pg.grid_w = int(grid_h), int(grid_w)
+    pg.n_sink, pg.window = int(n_sink), int(window)
+    return pg
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python pose_retrieved_kv_b200/build.py` (needs nvcc)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, ll, i, f = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_float
-    lp = ctypes.POINTER(Layout)
+    lp, pp = ctypes.POINTER(Layout), ctypes.POINTER(Paged)
     sig = {
         "prsink_version": ([], i),
         "prsink_last_error": ([], ctypes.c_char_p),
@@ -112,6 +139,12 @@ def _load():
                                       i, vp], i),
         "prsink_bank_update_policy": ([lp, ctypes.POINTER(BankPolicy), vp, vp, vp, i, vp, ll,
                                        vp, vp, vp, vp, i, vp], i),
+        "prsink_attention_backward": ([lp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp,
+                                       vp, ll, vp], i),
+        "prsink_attention_backward_scratch_bytes": ([lp], ll),
+        "prsink_paged_append": ([pp, vp, vp, ll, ll, vp, vp, vp, vp, i, vp, vp, ll, vp, vp], i),
+        "prsink_paged_attention": ([pp, vp, vp, vp, vp, vp, vp, vp, vp, ll, vp], i),
+        "prsink_paged_attention_scratch_bytes": ([pp], ll),
         "prsink_sync_status": ([vp], i),
         "prsink_debug_wait_timeout": ([ll, vp], i),
         "prsink_debug_attention_stall": ([ll], i),
@@ -133,7 +166,9 @@ def exported_symbols() -> list:
             "prsink_retrieve_fallback", "prsink_bank_update_policy", "prsink_attention_fused",
             "prsink_rotate_sinks", "prsink_debug_attention_stall", "prsink_attention_split",
             "prsink_attention_scratch_bytes", "prsink_attention_split_noalloc",
-            "prsink_attention_fused_split"]
+            "prsink_attention_fused_split", "prsink_attention_backward",
+            "prsink_attention_backward_scratch_bytes", "prsink_paged_append",
+            "prsink_paged_attention", "prsink_paged_attention_scratch_bytes"]
 
 
 def _check(rc: int, fn: str):
@@ -386,7 +421,8 @@ def prsink_bank_update_policy(layout: Optional[Layout], policy: BankPolicy, bank
 
 
 def prsink_sync_status(stream=None) -> int:
-    """Synchronise and return the status code (0 or PRSINK_ERR_TIMEOUT); does not raise."""
+    """Synchronise and return the status code (0, PRSINK_ERR_TIMEOUT or PRSINK_ERR_PAGE); does
+    not raise."""
     return _lib.prsink_sync_status(_stream(stream))
 
 
@@ -407,3 +443,115 @@ def prsink_attention_fused_split(layout: Layout, q, k_new, v_new, k_rot, k_cache
         raise ValueError("prsink_attention_fused_split needs scratch")
     prsink_attention_fused(layout, q, k_new, v_new, k_rot, k_cache, v_cache, out, lse, dyn_src,
                            stream, scratch=scratch)
+
+
+def _one_device(fn: str, **tensors):
+    """Every CUDA tensor on the current device (the one whose stream the call is given to)."""
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.is_cuda and \
+                t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{fn}: {name} is on {t.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+
+
+def prsink_attention_backward_scratch_bytes(layout: Layout) -> int:
+    n = _lib.prsink_attention_backward_scratch_bytes(ctypes.byref(layout))
+    if n < 0:
+        raise PRSinkError(PRSINK_ERR_ARG, "prsink_attention_backward_scratch_bytes",
+                          prsink_last_error())
+    return n
+
+
+def prsink_attention_backward(layout: Layout, q, k_cache, v_cache, out, lse, d_out, dq, dk, dv,
+                              scratch, dyn_src=None, grad_mask: int = 0xFFFFFFFF, stream=None):
+    """Gradient of ``prsink_attention`` for raw q, k and v; ``out`` and ``lse`` are the forward's.
+    ``scratch``: a uint8 CUDA tensor of prsink_attention_backward_scratch_bytes(layout) bytes.
+    ``dk`` / ``dv`` may be None when ``grad_mask`` selects no slot."""
+    _, lblk, _, T = prsink_layout_tokens(layout)
+    H, d = layout.n_heads, layout.head_dim
+    bf = torch.bfloat16
+    args = (_ptr(q, "q", bf, lblk * H * d), _ptr(k_cache, "k_cache", bf, H * T * d),
+            _ptr(v_cache, "v_cache", bf, H * T * d), _ptr(out, "out", bf, lblk * H * d),
+            _ptr(lse, "lse", torch.float32, H * lblk), _ptr(d_out, "d_out", bf, lblk * H * d),
+            _ptr(dq, "dq", bf, lblk * H * d), _ptr(dk, "dk", bf, H * T * d),
+            _ptr(dv, "dv", bf, H * T * d))
+    _one_device("prsink_attention_backward", q=q, k_cache=k_cache, v_cache=v_cache, out=out,
+                lse=lse, d_out=d_out, dq=dq, dk=dk, dv=dv, scratch=scratch, dyn_src=dyn_src)
+    rc = _lib.prsink_attention_backward(
+        ctypes.byref(layout), *args, int(grad_mask) & 0xFFFFFFFF,
+        _ptr(dyn_src, "dyn_src", torch.int64, 1), _ptr(scratch, "scratch", torch.uint8),
+        0 if scratch is None else int(scratch.numel()), _stream(stream))
+    _check(rc, "prsink_attention_backward")
+
+
+def _tokens(t, name: str, heads: int, d: int):
+    """Pointer, token stride and token count of ``t`` [n][heads][d]: rows of a wider buffer (a
+    fused projection's output) are fine, each row itself contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [n_tokens][{heads}][{d}], got {tuple(t.shape)}")
+    n = t.shape[0]
+    if n and ((heads > 1 and t.stride(1) != d) or t.stride(2) != 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.data_ptr(), (t.stride(0) if n > 1 else heads * d), n
+
+
+def _paged_sizes(paged: Paged, k_pages, v_pages, page_table, seq_lens):
+    n = paged.n_pages * paged.n_kv_heads * paged.page_size * paged.head_dim
+    return (_ptr(k_pages, "k_pages", torch.bfloat16, n),
+            _ptr(v_pages, "v_pages", torch.bfloat16, n),
+            _ptr(page_table, "page_table", torch.int32, paged.n_seqs * paged.max_pages),
+            _ptr(seq_lens, "seq_lens", torch.int32, paged.n_seqs))
+
+
+def prsink_paged_append(paged: Paged, k_new, v_new, k_pages, v_pages, page_table, seq_lens,
+                        cu_new=None, q=None, q_rot=None, stream=None):
+    """``k_new`` / ``v_new`` / ``q`` [n_tokens][heads][d], their token stride free;
+    ``cu_new`` int32 [n_seqs + 1] (None: one token per sequence)."""
+    kp, ks, n = _tokens(k_new, "k_new", paged.n_kv_heads, paged.head_dim)
+    vp, vs, nv = _tokens(v_new, "v_new", paged.n_kv_heads, paged.head_dim)
+    if nv != n:
+        raise ValueError(f"k_new holds {n} tokens, v_new {nv}")
+    qp, qs = 0, 0
+    if q is not None:
+        qp, qs, nq = _tokens(q, "q", paged.n_heads, paged.head_dim)
+        if nq != n:
+            raise ValueError(f"k_new holds {n} tokens, q {nq}")
+    pools = _paged_sizes(paged, k_pages, v_pages, page_table, seq_lens)
+    cu = _ptr(cu_new, "cu_new", torch.int32, paged.n_seqs + 1)
+    qr = _ptr(q_rot, "q_rot", torch.bfloat16, n * paged.n_heads * paged.head_dim)
+    _one_device("prsink_paged_append", k_new=k_new, v_new=v_new, k_pages=k_pages,
+                v_pages=v_pages, page_table=page_table, seq_lens=seq_lens, cu_new=cu_new, q=q,
+                q_rot=q_rot)
+    rc = _lib.prsink_paged_append(ctypes.byref(paged), kp, vp, ks, vs, *pools, n, cu, qp, qs, qr,
+                                  _stream(stream))
+    _check(rc, "prsink_paged_append")
+
+
+def prsink_paged_attention_scratch_bytes(paged: Paged) -> int:
+    n = _lib.prsink_paged_attention_scratch_bytes(ctypes.byref(paged))
+    if n < 0:
+        raise PRSinkError(PRSINK_ERR_ARG, "prsink_paged_attention_scratch_bytes",
+                          prsink_last_error())
+    return n
+
+
+def prsink_paged_attention(paged: Paged, q, k_pages, v_pages, page_table, seq_lens, out, scratch,
+                           lse=None, stream=None):
+    """``scratch``: a uint8 CUDA tensor of prsink_paged_attention_scratch_bytes(paged) bytes."""
+    n = paged.n_seqs * paged.n_heads
+    qp = _ptr(q, "q", torch.bfloat16, n * paged.head_dim)
+    pools = _paged_sizes(paged, k_pages, v_pages, page_table, seq_lens)
+    op = _ptr(out, "out", torch.bfloat16, n * paged.head_dim)
+    lp = _ptr(lse, "lse", torch.float32, n)
+    _one_device("prsink_paged_attention", q=q, k_pages=k_pages, v_pages=v_pages,
+                page_table=page_table, seq_lens=seq_lens, out=out, scratch=scratch, lse=lse)
+    rc = _lib.prsink_paged_attention(
+        ctypes.byref(paged), qp, *pools, op, lp, _ptr(scratch, "scratch", torch.uint8),
+        0 if scratch is None else int(scratch.numel()), _stream(stream))
+    _check(rc, "prsink_paged_attention")

@@ -158,7 +158,7 @@ using namespace prsink;
 
 extern "C" {
 
-int prsink_version(void) { return 2; }
+int prsink_version(void) { return 3; }
 
 const char* prsink_last_error(void) { return g_err; }
 
@@ -197,6 +197,10 @@ int prsink_sync_status(void* stream) {
     if (host & kStatusTimeout) {
       set_error("a bounded device wait ran out");
       return PRSINK_ERR_TIMEOUT;
+    }
+    if (host & kStatusPage) {
+      set_error("a paged call met a sequence length or page index out of range");
+      return PRSINK_ERR_PAGE;
     }
   }
   return PRSINK_OK;

@@ -37,6 +37,7 @@ int make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_
 // device side
 // ------------------------------------------------------------------------------------------
 constexpr int kStatusTimeout = 1;
+constexpr int kStatusPage = 2;            // length or page index out of range (paged calls)
 
 __device__ __forceinline__ uint64_t globaltimer() {
   uint64_t t;
