@@ -242,6 +242,7 @@ def _own(state):
             state["scratch"] = torch.empty(
                 P.prsink_attention_backward_scratch_bytes(state["layout"]), dtype=torch.uint8,
                 device="cuda")
+            state["out"] = state["out"].contiguous()
         P.prsink_attention_backward(state["layout"], state["q"], state["k"], state["v"],
                                     state["out"], state["lse"], state["d_out"], state["dq"],
                                     state["dk"], state["dv"], state["scratch"])
