@@ -175,59 +175,629 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
 }
 
 // --------------------------------------------------------------------------------- attention
-// One CTA per (sequence, query head); each warp walks every fourth key with a running maximum
-// and sum, lanes across the head dimension; the four warps are joined in shared memory.
-template <int D>
-__global__ void __launch_bounds__(128)
-paged_attention_kernel(const Cache cc, const __nv_bfloat16* q, const __nv_bfloat16* k_pages,
-                       const __nv_bfloat16* v_pages, __nv_bfloat16* out, float* lse,
-                       float scale_log2) {
-  constexpr int E = D / 32;
-  const int s = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = h / (cc.H / cc.Hkv);
-  const int len = seq_len(cc, s);
-  const int win0 = cc.window > 0 ? max(0, len - cc.window) : 0;
-  const long long qrow = (static_cast<long long>(s) * cc.H + h) * D;
-  float qv[E], acc[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) {
-    qv[e] = __bfloat162float(q[qrow + lane * E + e]) * scale_log2;
-    acc[e] = 0.f;
+// One new token per sequence: HBM-bound, every K and V byte is read once.  The tensor core takes
+// the products with the KEYS as the 128 rows of its tile and the query heads that share a key
+// head as its N columns, so K and V go from TMA straight to the MMA and no thread touches them:
+//   S^T [128 keys][N heads] = K Q^T        (A = K tile, K-major;  B = Q, N rows)
+//   O^T [d][N heads]       += V^T P^T      (A = V tile, MN-major; B = P, N rows of 128 keys)
+// The softmax between them handles 128 x N scores per tile: one key per thread as they come out
+// of tensor memory, transposed through shared memory to one head per warp (32 lanes x 4 keys),
+// running maximum and sum per head, P to shared memory as bf16.
+//
+// Work is cut into units of one key tile of one (sequence, key head) row, in row order; every
+// CTA (one per SM) takes an equal, contiguous share, so ragged lengths balance and one long
+// sequence spreads over the device.  A row shared by several CTAs leaves one partial result
+// (O, m, l) each in scratch; the last CTA to arrive joins them in CTA order.
+//
+// A tile holds whole pages up to 128 tokens, or up to 128 tokens of one page; one TMA box per
+// page.  Warps: 0-3 softmax, 4 TMA producer, 5 MMA issuer.
+constexpr int kTile = 128;                 // key rows of a tile = TMEM lanes
+constexpr int kAttThreads = 192;
+constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kMaxStages = 6;
+constexpr int kMetaRing = 16;              // tiles whose bad-page bits are kept
+constexpr float kRescale = 8.0f;           // log2 units: O is rescaled when a maximum grows > 2^8
+
+struct AttParams {
+  Cache c;
+  int group, chunks;                       // query heads per key head, N-column chunks of them
+  int tile_tokens;                         // tokens of a tile when pages are smaller than a tile
+  int tiles_per_page;                      // tiles of a page when pages are larger (else 0)
+  int box_rows;                            // rows of one TMA box (a page, or a tile)
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;                           // [CTAs][2][N][D] unnormalised partial results
+  float2* part_ml;                         // [CTAs][2][N] their maximum (log2 units) and sum
+  int* part_cnt;                           // [CTAs] arrivals per shared row (zero at launch)
+  unsigned long long timeout_ns;
+};
+
+template <int D, int N>
+struct Smem {
+  static constexpr int kTileBytes = kTile * D * 2;
+  // K and V stages: as many as fit beside Q, P and the scores
+  static constexpr int kKS = D == 128 ? (N == 64 ? 2 : 3) : (N == 16 ? 6 : (N == 32 ? 5 : 4));
+  static constexpr int kVS = D == 128 ? (N == 16 ? 3 : 2) : kKS;
+  // V first: the second 64-row panel that the MMA reads past a 64-wide V tile (rows of O^T that
+  // nobody uses) then stays inside the allocation
+  static constexpr int kV = 0;
+  static constexpr int kK = kV + kVS * kTileBytes;
+  static constexpr int kQ = kK + kKS * kTileBytes;      // 2 buffers
+  static constexpr int kP = kQ + 2 * N * D * 2;
+  static constexpr int kS = kP + N * kTile * 2;
+  static constexpr int kBytes = kS + N * kTile * 4;
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, N, false, false);
+  static constexpr uint32_t kIdescO = idesc_bf16_f32(128, N, true, false);
+  static constexpr uint32_t kColO = 2 * N;              // TMEM: S0, S1, O
+  static constexpr uint32_t kTmemCols = N == 16 ? 64 : (N == 32 ? 128 : 256);
+  static_assert(kKS <= kMaxStages && kKS + 2 < kMetaRing, "stages");
+  static_assert(kBytes + 1024 <= 227 * 1024, "shared memory");
+};
+
+// The attended tokens of a sequence and their tiles: tokens [0, sink) and [win0, len); tiles
+// [0, n_a) and [first_b, first_b + count - n_a).
+struct Row {
+  int len, sink, win0, n_a, first_b, count;
+  __device__ __forceinline__ static int tile_of(const AttParams& p, int token) {
+    if (!p.tiles_per_page) return token / p.tile_tokens;
+    const int page = token / p.c.page_size;
+    return page * p.tiles_per_page + (token - page * p.c.page_size) / kTile;
   }
-  for (int t = warp; t < len; t += 4) {
-    if (t >= cc.n_sink && t < win0) continue;
-    const int page = cc.table[static_cast<long long>(s) * cc.max_pages + t / cc.page_size];
-    if (page < 0 || page >= cc.n_pages) {
-      if (lane == 0) atomicOr(cc.status, kStatusPage);
-      continue;
+  __device__ __forceinline__ Row(const AttParams& p, int n) {
+    len = n;
+    win0 = p.c.window > 0 ? max(0, len - p.c.window) : 0;
+    sink = min(p.c.n_sink, win0);
+    n_a = sink > 0 ? tile_of(p, sink - 1) + 1 : 0;
+    first_b = 0;
+    count = 0;
+    if (len > 0) {
+      first_b = max(tile_of(p, win0), n_a);
+      count = n_a + max(0, tile_of(p, len - 1) + 1 - first_b);
     }
-    const long long row = ((static_cast<long long>(page) * cc.Hkv + kvh) * cc.page_size +
-                           t % cc.page_size) * D + lane * E;
-    float x = 0.f;
-    for (int e = 0; e < E; ++e) x += qv[e] * __bfloat162float(k_pages[row + e]);
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    const float mn = fmaxf(m, x), a = exp2f(m - mn), w = exp2f(x - mn);
-    l = l * a + w;
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * __bfloat162float(v_pages[row + e]);
-    m = mn;
   }
-  __shared__ float sm[4], sl[4], so[4][D];
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
-  if (lane == 0) { sm[warp] = m; sl[warp] = l; }
+  __device__ __forceinline__ bool attended(int token) const {
+    return token < sink || (token >= win0 && token < len);
+  }
+  // first token and tokens of the i-th attended tile
+  __device__ __forceinline__ void tile(const AttParams& p, int i, int& start, int& cnt) const {
+    const int t = i < n_a ? i : first_b + (i - n_a);
+    if (!p.tiles_per_page) {
+      start = t * p.tile_tokens;
+      cnt = p.tile_tokens;
+    } else {
+      const int page = t / p.tiles_per_page, sub = (t - page * p.tiles_per_page) * kTile;
+      start = page * p.c.page_size + sub;
+      cnt = min(kTile, p.c.page_size - sub);
+    }
+  }
+  // every token of a tile is attended
+  __device__ __forceinline__ bool whole(int start, int cnt) const {
+    return start + cnt <= sink || (start >= win0 && start + cnt <= len);
+  }
+};
+
+// A CTA's share of the units, row by row; every role walks it on its own.
+struct Walk {
+  long long left;                          // units left, this segment's included
+  int s, hc, i0, n;                        // sequence, head chunk, first tile, tiles here
+  Row row;
+  bool first;                              // the CTA's first segment
+  __device__ __forceinline__ Walk(const AttParams& p, int s0, long long off, long long units)
+      : left(units), s(s0), hc(0), i0(0), n(0), row(p, 0), first(true) {
+    if (left > 0) {
+      row = Row(p, seq_len(p.c, s));
+      if (row.count == 0) { left = 0; return; }            // (lengths changed under the call)
+      hc = static_cast<int>(off / row.count);
+      i0 = static_cast<int>(off - static_cast<long long>(hc) * row.count);
+      take();
+    }
+  }
+  __device__ __forceinline__ void take() {
+    n = static_cast<int>(min(left, static_cast<long long>(row.count - i0)));
+  }
+  __device__ __forceinline__ void next(const AttParams& p) {
+    left -= n;
+    first = false;
+    if (left <= 0) return;
+    i0 = 0;
+    if (++hc == p.c.Hkv * p.chunks) {
+      hc = 0;
+      do {
+        if (++s >= p.c.n_seqs) { left = 0; return; }       // (lengths changed under the call)
+        row = Row(p, seq_len(p.c, s));
+      } while (row.count == 0);
+    }
+    take();
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 consecutive 32-bit columns of this thread's lane -> registers.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+enum Bar {
+  B_KFULL = 0, B_KEMPTY = B_KFULL + kMaxStages, B_VFULL = B_KEMPTY + kMaxStages,
+  B_VEMPTY = B_VFULL + kMaxStages, B_SFULL = B_VEMPTY + kMaxStages, B_SEMPTY = B_SFULL + 2,
+  B_QFULL = B_SEMPTY + 2, B_QEMPTY = B_QFULL + 2, B_PFULL = B_QEMPTY + 2, B_PVDONE, B_FINAL,
+  B_COUNT
+};
+
+// Bounded wait that ignores the abort flag (used while draining after an abort).
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t dl = globaltimer() + 100000000ull;
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() > dl) break;
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(kAttThreads, 1)
+paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ AttParams p) {
+  using SM = Smem<D, N>;
+  extern __shared__ uint8_t dsmem[];
+  __shared__ __align__(8) uint64_t bars[B_COUNT];
+  __shared__ uint32_t tmem_base_s;
+  __shared__ AbortState ab;
+  __shared__ uint16_t bad_pages[kMetaRing];
+  __shared__ float alpha_s[N], m_s[N], l_s[N];
+  __shared__ long long scan_s[kAttThreads / 32], total_s, off_s;
+  __shared__ int start_s, last_s;
+  __shared__ int loads_s[3];                       // Q, K and V loads sent (for the drain)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = smem_u32(dsmem);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* gb = dsmem + (sb - raw);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(bar(B_KFULL + i), 1);
+      mbar_init(bar(B_KEMPTY + i), 1);
+      mbar_init(bar(B_VFULL + i), 1);
+      mbar_init(bar(B_VEMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_SFULL + i), 1);
+      mbar_init(bar(B_SEMPTY + i), 128);
+      mbar_init(bar(B_QFULL + i), 1);
+      mbar_init(bar(B_QEMPTY + i), 1);
+    }
+    mbar_init(bar(B_PFULL), 128);
+    mbar_init(bar(B_PVDONE), 1);
+    mbar_init(bar(B_FINAL), 1);
+    ab.flag = 0;
+    start_s = 0;
+    off_s = 0;
+    loads_s[0] = loads_s[1] = loads_s[2] = 0;
+    fence_barrier_init();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&tmem_base_s), SM::kTmemCols);
+    tmem_relinquish();
+  }
+  // columns of P that no head fills must be finite; V rows that no box fills (pages that do not
+  // divide a tile) too: P is 0 there, but 0 * NaN is not
+  for (int i = threadIdx.x; i < N * kTile * 2 / 16; i += kAttThreads)
+    reinterpret_cast<uint4*>(gb + SM::kP)[i] = make_uint4(0, 0, 0, 0);
+  if (!p.tiles_per_page && p.tile_tokens < kTile)
+    for (int i = threadIdx.x; i < SM::kVS * SM::kTileBytes / 16; i += kAttThreads)
+      reinterpret_cast<uint4*>(gb + SM::kV)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  // units before each sequence: a block-wide scan, `per` consecutive sequences per thread
+  const int hcs = p.c.Hkv * p.chunks;
+  const int per = (p.c.n_seqs + kAttThreads - 1) / kAttThreads;
+  const int sa = min(p.c.n_seqs, static_cast<int>(threadIdx.x) * per);
+  const int se = min(p.c.n_seqs, sa + per);
+  long long mine = 0;
+  for (int s = sa; s < se; ++s) mine += static_cast<long long>(Row(p, seq_len(p.c, s)).count) * hcs;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) scan_s[warp] = incl;
   __syncthreads();
-  const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float L = 0.f, w[4];
-  for (int i = 0; i < 4; ++i) {
-    w[i] = sm[i] > -INFINITY ? exp2f(sm[i] - M) : 0.f;
-    L += w[i] * sl[i];
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kAttThreads / 32; ++w) {
+    if (w < warp) before += scan_s[w];
+    total += scan_s[w];
   }
-  if (threadIdx.x < D) {
-    float o = 0.f;
-    for (int i = 0; i < 4; ++i) o += w[i] * so[i][threadIdx.x];
-    out[qrow + threadIdx.x] = __float2bfloat16_rn(L > 0.f ? o / L : 0.f);
+  // CTAs that have work: no more than units, so that each of them has at least one
+  const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1ll)));
+  const int cta = blockIdx.x;
+  const long long u0 = cta < G ? total * cta / G : total;
+  const long long u1 = cta < G ? total * (cta + 1) / G : total;
+  if (u0 >= before && u0 < before + mine) {        // this thread's sequences hold the first unit
+    long long off = u0 - before;
+    for (int s = sa; s < se; ++s) {
+      const long long n = static_cast<long long>(Row(p, seq_len(p.c, s)).count) * hcs;
+      if (off < n) {
+        start_s = s;
+        off_s = off;
+        break;
+      }
+      off -= n;
+    }
   }
-  if (lse && threadIdx.x == 0)
-    lse[static_cast<long long>(s) * cc.H + h] =
-        L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  const uint64_t deadline = globaltimer() + p.timeout_ns;
+  Walk w(p, start_s, off_s, u1 - u0);
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------------- TMA producer
+    // K(j), then V(j - 1): the order in which the MMA warp takes them.  Lane i loads page i of
+    // the tile; pages without an attended token are left alone (their rows are masked).
+    int j = 0, seg = 0;
+    bool ok = true;
+    int v_c2 = -1, v_row = 0, v_np = 0;            // the previous tile's boxes
+    auto load = [&](int full, uint32_t dst, const CUtensorMap* tm, int c2, int row, int np) {
+      if (lane == 0) mbar_arrive_expect_tx(bar(full), np * p.box_rows * D * 2);
+      __syncwarp();
+      if (c2 >= 0)
+        for (int pp = 0; pp < D / 64; ++pp)
+          tma_load_3d(dst + pp * (kTile * 128) + (p.tiles_per_page ? 0 : lane * p.box_rows * 128),
+                      tm, bar(full), pp * 64, row, c2);
+    };
+    auto load_v = [&](int jv) {
+      const int st = jv % SM::kVS;
+      if (jv >= SM::kVS)
+        ok = mbar_wait(bar(B_VEMPTY + st), (jv / SM::kVS - 1) & 1, &ab, deadline, p.c.status);
+      if (!__all_sync(~0u, ok)) { ok = false; return; }
+      load(B_VFULL + st, sb + SM::kV + st * SM::kTileBytes, &tm_v, v_c2, v_row, v_np);
+      if (lane == 0) loads_s[2] = jv + 1;
+    };
+    for (; ok && w.left > 0; w.next(p), ++seg) {
+      const int* table = p.c.table + static_cast<long long>(w.s) * p.c.max_pages;
+      const int kvh = w.hc / p.chunks, chunk = w.hc - kvh * p.chunks;
+      if (seg >= 2)
+        ok = mbar_wait(bar(B_QEMPTY + (seg & 1)), ((seg >> 1) - 1) & 1, &ab, deadline, p.c.status);
+      if (!__all_sync(~0u, ok)) { ok = false; break; }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(B_QFULL + (seg & 1)), N * D * 2);
+        for (int pp = 0; pp < D / 64; ++pp)
+          tma_load_3d(sb + SM::kQ + (seg & 1) * N * D * 2 + pp * N * 128, &tm_q,
+                      bar(B_QFULL + (seg & 1)), pp * 64, chunk * N, w.s * p.c.Hkv + kvh);
+        loads_s[0] = seg + 1;
+      }
+      for (int i = 0; ok && i < w.n; ++i, ++j) {
+        int start, cnt;
+        w.row.tile(p, w.i0 + i, start, cnt);
+        // this lane's page
+        const int first = p.tiles_per_page ? start : start + lane * p.c.page_size;
+        const int page_no = start / p.c.page_size + (p.tiles_per_page ? 0 : lane);
+        bool need = p.tiles_per_page ? lane == 0 : lane * p.c.page_size < cnt;
+        need = need && (first < w.row.sink ||
+                        (first + p.c.page_size > w.row.win0 && first < w.row.len));
+        int c2 = -1;
+        bool bad = false;
+        if (need) {
+          int page = table[page_no];
+          bad = page < 0 || page >= p.c.n_pages;
+          if (bad) page = p.c.n_pages;             // past the pool: the box is filled with zeros
+          c2 = bad ? page * p.c.Hkv : page * p.c.Hkv + kvh;
+        }
+        const uint32_t bad_mask = __ballot_sync(~0u, bad);
+        if (bad_mask && lane == 0) atomicOr(p.c.status, kStatusPage);
+        const int np = __popc(__ballot_sync(~0u, need));
+        const int row = p.tiles_per_page ? start - page_no * p.c.page_size : 0;
+        const int st = j % SM::kKS;
+        if (j >= SM::kKS)
+          ok = mbar_wait(bar(B_KEMPTY + st), (j / SM::kKS - 1) & 1, &ab, deadline, p.c.status);
+        if (!__all_sync(~0u, ok)) { ok = false; break; }
+        if (lane == 0) bad_pages[j & (kMetaRing - 1)] = static_cast<uint16_t>(bad_mask);
+        load(B_KFULL + st, sb + SM::kK + st * SM::kTileBytes, &tm_k, c2, row, np);
+        if (lane == 0) loads_s[1] = j + 1;
+        if (j > 0) load_v(j - 1);
+        v_c2 = c2;
+        v_row = row;
+        v_np = np;
+      }
+    }
+    if (ok && j > 0) load_v(j - 1);
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      int j = 0, seg = 0;
+      bool ok = true, prev_first = false;
+      auto pv = [&](int jv, bool first_of_segment) -> bool {
+        const int st = jv % SM::kVS;
+        if (!mbar_wait(bar(B_VFULL + st), (jv / SM::kVS) & 1, &ab, deadline, p.c.status) ||
+            !mbar_wait(bar(B_PFULL), jv & 1, &ab, deadline, p.c.status))
+          return false;
+        tc_fence_after();
+        const uint64_t a = sdesc_sw128(sb + SM::kV + st * SM::kTileBytes, kTile * 128, 1024);
+        const uint64_t b = sdesc_sw128(sb + SM::kP, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ss(tmem + SM::kColO, a + kk * 128, b + (kk >> 2) * (N * 8) + (kk & 3) * 2,
+                  SM::kIdescO, !(first_of_segment && kk == 0));
+        umma_commit(bar(B_VEMPTY + st));
+        umma_commit(bar(B_PVDONE));
+        return true;
+      };
+      for (; ok && w.left > 0; w.next(p), ++seg) {
+        ok = mbar_wait(bar(B_QFULL + (seg & 1)), (seg >> 1) & 1, &ab, deadline, p.c.status);
+        const uint64_t b = sdesc_sw128(sb + SM::kQ + (seg & 1) * N * D * 2, 16, 1024);
+        for (int i = 0; ok && i < w.n; ++i, ++j) {
+          const int st = j % SM::kKS, sbuf = j & 1;
+          ok = mbar_wait(bar(B_KFULL + st), (j / SM::kKS) & 1, &ab, deadline, p.c.status) &&
+               (j < 2 || mbar_wait(bar(B_SEMPTY + sbuf), ((j >> 1) - 1) & 1, &ab, deadline,
+                                   p.c.status));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = sdesc_sw128(sb + SM::kK + st * SM::kTileBytes, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(tmem + sbuf * N, a + (kk >> 2) * 1024 + (kk & 3) * 2,
+                    b + (kk >> 2) * (N * 8) + (kk & 3) * 2, SM::kIdescS, kk != 0);
+          umma_commit(bar(B_SFULL + sbuf));
+          umma_commit(bar(B_KEMPTY + st));
+          if (i + 1 == w.n) umma_commit(bar(B_QEMPTY + (seg & 1)));
+          if (j > 0) ok = pv(j - 1, prev_first);
+          prev_first = i == 0;
+        }
+      }
+      if (ok && j > 0) pv(j - 1, prev_first);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------- softmax (warps 0-3)
+    const int t = threadIdx.x;                     // key row = TMEM lane; O^T: element of d
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    float* sc = reinterpret_cast<float*>(gb + SM::kS);
+    constexpr int HW = N / 4;                      // heads of a warp: warp, warp + 4, ...
+    // sequences with nothing to attend
+    for (int s = cta; s < p.c.n_seqs; s += gridDim.x) {
+      if (Row(p, seq_len(p.c, s)).count) continue;
+      uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<long long>(s) * p.c.H * D);
+      for (int i = t; i < p.c.H * D / 8; i += 128) o[i] = make_uint4(0, 0, 0, 0);
+      if (p.lse)
+        for (int i = t; i < p.c.H; i += 128)
+          p.lse[static_cast<long long>(s) * p.c.H + i] = -INFINITY;
+    }
+    int j = 0;
+    bool ok = true;
+    for (; ok && w.left > 0; w.next(p)) {
+      const int kvh = w.hc / p.chunks, chunk = w.hc - kvh * p.chunks;
+      const int nh = min(N, p.group - chunk * N);  // heads of this chunk
+      float m[HW], l[HW];
+#pragma unroll
+      for (int i = 0; i < HW; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
+      for (int i = 0; i < w.n; ++i, ++j) {
+        int start, cnt;
+        w.row.tile(p, w.i0 + i, start, cnt);
+        ok = mbar_wait(bar(B_SFULL + (j & 1)), (j >> 1) & 1, &ab, deadline, p.c.status);
+        if (!named_bar_and(1, 128, ok)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s[N];
+        if constexpr (N == 16) {
+          tmem_ld16(tmem + lane_off + (j & 1) * N, *reinterpret_cast<uint32_t(*)[16]>(&s[0]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < N; c += 32)
+            tmem_ld32(tmem + lane_off + (j & 1) * N + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
+        }
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(bar(B_SEMPTY + (j & 1)));
+        const uint32_t bad = bad_pages[j & (kMetaRing - 1)];
+        bool live = t < cnt && w.row.attended(start + t);
+        if (bad) live = live && !((bad >> (p.tiles_per_page ? 0 : t / p.c.page_size)) & 1u);
+#pragma unroll
+        for (int g = 0; g < N; ++g)
+          if (g < nh) sc[g * kTile + t] = live ? __uint_as_float(s[g]) : -INFINITY;
+        named_bar_sync(1, 128);
+        bool grown = false;
+        uint2 pk[HW];
+#pragma unroll
+        for (int k = 0; k < HW; ++k) {
+          const int g = warp + 4 * k;
+          if (g >= nh) break;
+          const float4 x = *reinterpret_cast<const float4*>(sc + g * kTile + 4 * lane);
+          float mt = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+#pragma unroll
+          for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, o));
+          mt *= p.scale_log2;
+          float alpha = 1.f;
+          if (mt > m[k] + kRescale || m[k] == -INFINITY) {   // -inf: nothing attended so far
+            if (m[k] > -INFINITY) {
+              alpha = ex2(m[k] - mt);
+              grown = true;
+            }
+            m[k] = mt;
+          }
+          const float me = m[k] > -INFINITY ? m[k] : 0.f;
+          const float4 e = make_float4(
+              ex2(fmaf(x.x, p.scale_log2, -me)), ex2(fmaf(x.y, p.scale_log2, -me)),
+              ex2(fmaf(x.z, p.scale_log2, -me)), ex2(fmaf(x.w, p.scale_log2, -me)));
+          l[k] = l[k] * alpha + ((e.x + e.y) + (e.z + e.w));
+          pk[k] = make_uint2(pack2(e.x, e.y), pack2(e.z, e.w));
+          if (lane == 0) alpha_s[g] = alpha;
+        }
+        // P(j - 1) V(j - 1) is done: P may be overwritten, O rescaled
+        if (j > 0) ok = mbar_wait(bar(B_PVDONE), (j - 1) & 1, &ab, deadline, p.c.status);
+#pragma unroll
+        for (int k = 0; k < HW; ++k) {
+          const int g = warp + 4 * k;
+          if (g >= nh) break;
+          const int byte = (8 * lane) & 127;
+          *reinterpret_cast<uint2*>(gb + SM::kP + (lane >> 4) * (N * 128) + g * 128 +
+                                    (((byte >> 4) ^ (g & 7)) << 4) + (byte & 15)) = pk[k];
+        }
+        if (!w.row.whole(start, cnt)) {
+          // rows without an attended token may hold anything
+          ok = ok && mbar_wait(bar(B_VFULL + j % SM::kVS), (j / SM::kVS) & 1, &ab, deadline,
+                               p.c.status);
+          if (!live && t < cnt)
+            for (int c = 0; c < D / 8; ++c)
+              *reinterpret_cast<uint4*>(gb + SM::kV + (j % SM::kVS) * SM::kTileBytes +
+                                        (c >> 3) * (kTile * 128) + t * 128 + ((c & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+        }
+        const bool same = named_bar_and(1, 128, !grown);
+        if (!same && i > 0) {
+          tc_fence_after();
+          constexpr int CH = N < 32 ? 16 : 32;
+#pragma unroll 1
+          for (int c = 0; c < N; c += CH) {
+            uint32_t o[CH];
+            const uint32_t at = tmem + lane_off + SM::kColO + c;
+            if constexpr (CH == 16) tmem_ld16(at, o); else tmem_ld32(at, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < CH; ++e)
+              if (c + e < nh) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_s[c + e]);
+            if constexpr (CH == 16) tmem_st16(at, o); else tmem_st32(at, o);
+          }
+          tmem_wait_st();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(B_PFULL));
+      }
+      // the row's result, or this CTA's part of it
+      if (ok) ok = mbar_wait(bar(B_PVDONE), (j - 1) & 1, &ab, deadline, p.c.status);
+      if (!named_bar_and(1, 128, ok)) { ok = false; break; }
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < HW; ++k) {
+        const int g = warp + 4 * k;
+        if (g >= nh) break;
+        float x = l[k];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+        if (lane == 0) {
+          m_s[g] = m[k];
+          l_s[g] = x;
+        }
+      }
+      uint32_t o[N];
+      if constexpr (N == 16) {
+        tmem_ld16(tmem + lane_off + SM::kColO, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+      } else {
+#pragma unroll
+        for (int c = 0; c < N; c += 32)
+          tmem_ld32(tmem + lane_off + SM::kColO + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c]));
+      }
+      tmem_wait_ld();
+      tc_fence_before();
+      named_bar_sync(1, 128);
+      const long long head0 = static_cast<long long>(w.s) * p.c.H + kvh * p.group + chunk * N;
+      if (w.n == w.row.count) {
+        if (t < D) {
+#pragma unroll
+          for (int g = 0; g < N; ++g)
+            if (g < nh)
+              p.out[(head0 + g) * D + t] = __float2bfloat16_rn(
+                  l_s[g] > 0.f ? __uint_as_float(o[g]) / l_s[g] : 0.f);
+        }
+        if (p.lse && t < nh)
+          p.lse[head0 + t] =
+              l_s[t] > 0.f ? (m_s[t] + log2f(l_s[t])) * 0.69314718055994530942f : -INFINITY;
+        continue;
+      }
+      const long long slot = (static_cast<long long>(cta) * 2 + (w.first ? 0 : 1)) * N;
+      if (t < D) {
+#pragma unroll
+        for (int g = 0; g < N; ++g)
+          if (g < nh) p.part_o[(slot + g) * D + t] = __uint_as_float(o[g]);
+      }
+      if (t < nh) p.part_ml[slot + t] = make_float2(m_s[t], l_s[t]);
+      __threadfence();
+      // the CTAs of this row: units [a, a + count); its counter is the last one's, for which no
+      // other shared row can be the one that started before it
+      const long long a = u1 - w.left - w.i0;
+      const int c0 = static_cast<int>(((a + 1) * G - 1) / total);
+      const int c1 = static_cast<int>(((a + w.row.count) * G - 1) / total);
+      named_bar_sync(1, 128);
+      if (t == 0) last_s = atomicAdd(&p.part_cnt[c1], 1) == c1 - c0;
+      named_bar_sync(1, 128);
+      if (!last_s) continue;
+      __threadfence();
+      // M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L, in CTA order
+      const bool aligned = total * c0 / G == a;    // the row's first CTA starts with it
+      for (int g = 0; g < nh; ++g) {
+        auto part = [&](int c) {
+          return (static_cast<long long>(c) * 2 + (c > c0 || aligned ? 0 : 1)) * N + g;
+        };
+        float M = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(&p.part_ml[part(c)]).x);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+        float L = 0.f, acc = 0.f;
+        for (int cb = c0; cb <= c1; cb += 32) {
+          float wt = 0.f;
+          if (cb + lane <= c1) {
+            const float2 ml = __ldcg(&p.part_ml[part(cb + lane)]);
+            wt = ml.x > -INFINITY ? ex2(ml.x - M) : 0.f;
+            L += wt * ml.y;
+          }
+          const int n = min(32, c1 - cb + 1);
+#pragma unroll 4
+          for (int c = 0; c < n; ++c) {
+            const float wc = __shfl_sync(~0u, wt, c);
+            if (t < D) acc += wc * __ldcg(&p.part_o[part(cb + c) * D + t]);
+          }
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+        if (t < D) p.out[(head0 + g) * D + t] = __float2bfloat16_rn(L > 0.f ? acc / L : 0.f);
+        if (p.lse && t == 0)
+          p.lse[head0 + g] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (ab.flag) {
+    // something gave up: the copies and MMAs in flight end before their memory is released
+    if (warp == kMmaWarp && lane == 0) {
+      umma_commit(bar(B_FINAL));
+      drain_wait(bar(B_FINAL), 0);
+      for (int i = max(0, loads_s[0] - 2); i < loads_s[0]; ++i)
+        drain_wait(bar(B_QFULL + (i & 1)), (i >> 1) & 1);
+      for (int i = max(0, loads_s[1] - SM::kKS); i < loads_s[1]; ++i)
+        drain_wait(bar(B_KFULL + i % SM::kKS), (i / SM::kKS) & 1);
+      for (int i = max(0, loads_s[2] - SM::kVS); i < loads_s[2]; ++i)
+        drain_wait(bar(B_VFULL + i % SM::kVS), (i / SM::kVS) & 1);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, SM::kTmemCols);
+  }
 }
 
 // ---------------------------------------------------------------------------------- host side
@@ -309,6 +879,52 @@ static int check_ptrs(const char* what, std::initializer_list<const void*> bufs,
 template <int D>
 static void launch_append(const AppendParams& p, cudaStream_t st) {
   paged_append_kernel<D, 1><<<dim3(p.n_tokens, 1), kAppendThreads, 0, st>>>(p);
+}
+
+// Columns of the score tile (query heads of a key head, in chunks of at most 64), CTAs and
+// scratch of an attention call.
+struct AttPlan {
+  int N, grid;
+  size_t ml, o, total;                     // byte offsets behind the counters; all 256-aligned
+};
+
+static AttPlan att_plan(const Cache& c, int D) {
+  AttPlan a{};
+  const int group = c.H / c.Hkv;
+  a.N = group <= 16 ? 16 : (group <= 32 ? 32 : 64);
+  int n_sm = 148, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  a.grid = n_sm;
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t parts = static_cast<size_t>(a.grid) * 2 * a.N;
+  a.ml = up(a.grid * sizeof(int));
+  a.o = a.ml + up(parts * sizeof(float2));
+  a.total = a.o + up(parts * D * sizeof(float));
+  return a;
+}
+
+template <int D_, int N_>
+struct Shape {
+  static constexpr int d = D_, n = N_;
+};
+
+template <int D, int N>
+static int launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                            const AttParams& p, int grid, cudaStream_t st) {
+  const int smem = Smem<D, N>::kBytes + 1024;
+  static bool allowed[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !allowed[dev]) {
+    if (cudaFuncSetAttribute(paged_attention_kernel<D, N>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return check_launch("prsink_paged_attention");
+    if (dev >= 0 && dev < 64) allowed[dev] = true;
+  }
+  paged_attention_kernel<D, N><<<grid, kAttThreads, smem, st>>>(mq, mk, mv, p);
+  count_launch();
+  return check_launch("prsink_paged_attention");
 }
 
 }  // namespace paged
@@ -395,7 +1011,7 @@ extern "C" long long prsink_paged_attention_scratch_bytes(const prsink_paged* pa
   using namespace prsink::paged;
   Cache c;
   if (check(paged, "prsink_paged_attention_scratch_bytes", &c)) return -1;
-  return 0;
+  return static_cast<long long>(att_plan(c, paged->head_dim).total);
 }
 
 extern "C" int prsink_paged_attention(const prsink_paged* paged, const void* q,
@@ -405,32 +1021,57 @@ extern "C" int prsink_paged_attention(const prsink_paged* paged, const void* q,
                                       void* stream) {
   using namespace prsink::paged;
   const char* what = "prsink_paged_attention";
-  Cache c;
-  int rc = check(paged, what, &c);
+  AttParams p{};
+  int rc = check(paged, what, &p.c);
   if (rc) return rc;
-  if (c.n_seqs == 0) return PRSINK_OK;
+  if (p.c.n_seqs == 0) return PRSINK_OK;
   rc = check_ptrs(what, {q, k_pages, v_pages, out}, {page_table, seq_lens});
   if (rc) return rc;
   if (reinterpret_cast<uintptr_t>(lse) & 3u) {
     set_error("%s: lse must be 4-byte aligned", what);
     return PRSINK_ERR_ALIGN;
   }
-  c.table = page_table;
-  c.lens = seq_lens;
-  c.status = status_word_ptr();
-  if (!c.status) return PRSINK_ERR_LAUNCH;
-  const float scale_log2 =
-      static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(paged->head_dim)));
+  const int D = paged->head_dim;
+  const AttPlan pl = att_plan(p.c, D);
+  if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) ||
+      scratch_bytes < static_cast<long long>(pl.total)) {
+    set_error("%s: scratch must be 256-byte aligned and hold %zu bytes (got %lld)", what, pl.total,
+              scratch_bytes);
+    return PRSINK_ERR_ARG;
+  }
+  p.c.table = page_table;
+  p.c.lens = seq_lens;
+  p.c.status = status_word_ptr();
+  if (!p.c.status) return PRSINK_ERR_LAUNCH;
+  p.group = p.c.H / p.c.Hkv;
+  p.chunks = (p.group + pl.N - 1) / pl.N;
+  const int ps = p.c.page_size;
+  p.tiles_per_page = ps < kTile ? 0 : (ps + kTile - 1) / kTile;
+  p.tile_tokens = ps < kTile ? kTile / ps * ps : kTile;
+  p.box_rows = ps < kTile ? ps : kTile;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.timeout_ns = 2000000000ull;
+  char* base = static_cast<char*>(scratch);
+  p.part_cnt = reinterpret_cast<int*>(base);
+  p.part_ml = reinterpret_cast<float2*>(base + pl.ml);
+  p.part_o = reinterpret_cast<float*>(base + pl.o);
+  CUtensorMap mq, mk, mv;
+  const uint64_t rows = static_cast<uint64_t>(p.c.n_pages) * p.c.Hkv;
+  rc = make_map(&mq, q, D, p.group, static_cast<uint64_t>(p.c.n_seqs) * p.c.Hkv, 2ull * D,
+                2ull * D * p.group, pl.N, 1);
+  if (!rc) rc = make_map(&mk, k_pages, D, ps, rows, 2ull * D, 2ull * D * ps, p.box_rows, 1);
+  if (!rc) rc = make_map(&mv, v_pages, D, ps, rows, 2ull * D, 2ull * D * ps, p.box_rows, 1);
+  if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(c.n_seqs, c.H);
-  auto launch = [&](auto kernel) {
-    kernel<<<grid, 128, 0, st>>>(c, static_cast<const __nv_bfloat16*>(q),
-                                 static_cast<const __nv_bfloat16*>(k_pages),
-                                 static_cast<const __nv_bfloat16*>(v_pages),
-                                 static_cast<__nv_bfloat16*>(out), lse, scale_log2);
-  };
-  if (paged->head_dim == 128) launch(paged_attention_kernel<128>);
-  else launch(paged_attention_kernel<64>);
-  count_launch();
-  return check_launch(what);
+  if (cudaMemsetAsync(p.part_cnt, 0, pl.grid * sizeof(int), st) != cudaSuccess)
+    return check_launch(what);
+  auto go = [&](auto tag) { return launch_attention<decltype(tag)::d, decltype(tag)::n>(
+      mq, mk, mv, p, pl.grid, st); };
+  if (D == 128)
+    return pl.N == 16 ? go(Shape<128, 16>{}) : pl.N == 32 ? go(Shape<128, 32>{})
+                                                          : go(Shape<128, 64>{});
+  return pl.N == 16 ? go(Shape<64, 16>{}) : pl.N == 32 ? go(Shape<64, 32>{})
+                                                       : go(Shape<64, 64>{});
 }

@@ -82,6 +82,8 @@ def test_paged_pointers_strides_and_counts():
     for name in ("table", "lens", "lse"):
         assert _attend(pg, **{name: 18}) == P.PRSINK_ERR_ALIGN
     empty = P.make_paged(**{**GOOD, "n_seqs": 0})
+    assert _attend(pg, scratch=None) == _attend(pg, scratch=128) == P.PRSINK_ERR_ARG
+    assert _attend(pg, nb=P.prsink_paged_attention_scratch_bytes(pg) - 1) == P.PRSINK_ERR_ARG
     assert _attend(empty) == P.PRSINK_OK and _append(empty, n=0) == P.PRSINK_OK
     assert P.prsink_launch_count() == before
 
