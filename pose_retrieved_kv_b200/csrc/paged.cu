@@ -29,7 +29,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // Length of sequence s, clamped to the table's capacity (out of range: recorded).
 __device__ __forceinline__ int seq_len(const Cache& c, int s) {
-  const int n = c.lens[s];
+  const int n = __ldcg(c.lens + s);
   if (n >= 0 && n <= c.capacity) return n;
   atomicOr(c.status, kStatusPage);
   return n < 0 ? 0 : c.capacity;
@@ -180,20 +180,24 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
 // head as its N columns, so K and V go from TMA straight to the MMA and no thread touches them:
 //   S^T [128 keys][N heads] = K Q^T        (A = K tile, K-major;  B = Q, N rows)
 //   O^T [d][N heads]       += V^T P^T      (A = V tile, MN-major; B = P, N rows of 128 keys)
-// The softmax between them handles 128 x N scores per tile: one key per thread as they come out
-// of tensor memory, transposed through shared memory to one head per warp (32 lanes x 4 keys),
-// running maximum and sum per head, P to shared memory as bf16.
+// The softmax between them has one key per thread.  Its running maximum m is only an offset: any
+// m within 2^8 of the true one keeps every probability in range, so a tile whose scores stay
+// below m + 8 (log2 units) needs no reduction at all, just one vote; the sums stay per thread
+// until the row ends.  A tile that exceeds it (and the first one of a row) takes the maximum
+// across the threads, and O and the sums are rescaled.
 //
 // Work is cut into units of one key tile of one (sequence, key head) row, in row order; every
 // CTA (one per SM) takes an equal, contiguous share, so ragged lengths balance and one long
 // sequence spreads over the device.  A row shared by several CTAs leaves one partial result
-// (O, m, l) each in scratch; the last CTA to arrive joins them in CTA order.
+// (O, m, l) each in scratch; a second kernel, launched early and waiting for the first, joins
+// them in CTA order (no counters to clear, no order that depends on timing).
 //
 // A tile holds whole pages up to 128 tokens, or up to 128 tokens of one page; one TMA box per
-// page.  Warps: 0-3 softmax, 4 TMA producer, 5 MMA issuer.
+// page.  Warps: 0-3 softmax, 4 TMA producer, 5 issues the S products, 6 the O products (one
+// thread issues an MMA in about 45 cycles whatever its size: a tile's 16 small ones are shared).
 constexpr int kTile = 128;                 // key rows of a tile = TMEM lanes
-constexpr int kAttThreads = 192;
-constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kAttThreads = 224;
+constexpr int kProducerWarp = 4, kScoreWarp = 5, kOutWarp = 6;
 constexpr int kMaxStages = 6;
 constexpr int kMetaRing = 16;              // tiles whose bad-page bits are kept
 constexpr float kRescale = 8.0f;           // log2 units: O is rescaled when a maximum grows > 2^8
@@ -201,15 +205,18 @@ constexpr float kRescale = 8.0f;           // log2 units: O is rescaled when a m
 struct AttParams {
   Cache c;
   int group, chunks;                       // query heads per key head, N-column chunks of them
-  int tile_tokens;                         // tokens of a tile when pages are smaller than a tile
+  int tile_tokens, pages_per_tile;         // of a tile when pages are smaller than a tile
   int tiles_per_page;                      // tiles of a page when pages are larger (else 0)
   int box_rows;                            // rows of one TMA box (a page, or a tile)
+  // K / V tiles in shared memory, in 1 KB swizzle atoms of 8 rows x 64 elements: bytes between
+  // row groups and between the two 64-element panels of a row
+  int group_bytes, panel_bytes;
+  bool one_box;                            // a box lands both panels (5-D map)
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
   float* part_o;                           // [CTAs][2][N][D] unnormalised partial results
   float2* part_ml;                         // [CTAs][2][N] their maximum (log2 units) and sum
-  int* part_cnt;                           // [CTAs] arrivals per shared row (zero at launch)
   unsigned long long timeout_ns;
 };
 
@@ -225,8 +232,8 @@ struct Smem {
   static constexpr int kK = kV + kVS * kTileBytes;
   static constexpr int kQ = kK + kKS * kTileBytes;      // 2 buffers
   static constexpr int kP = kQ + 2 * N * D * 2;
-  static constexpr int kS = kP + N * kTile * 2;
-  static constexpr int kBytes = kS + N * kTile * 4;
+  static constexpr int kPBytes = N * kTile * 2;         // 2 buffers
+  static constexpr int kBytes = kP + 2 * kPBytes;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(128, N, false, false);
   static constexpr uint32_t kIdescO = idesc_bf16_f32(128, N, true, false);
   static constexpr uint32_t kColO = 2 * N;              // TMEM: S0, S1, O
@@ -259,23 +266,67 @@ struct Row {
   __device__ __forceinline__ bool attended(int token) const {
     return token < sink || (token >= win0 && token < len);
   }
-  // first token and tokens of the i-th attended tile
-  __device__ __forceinline__ void tile(const AttParams& p, int i, int& start, int& cnt) const {
-    const int t = i < n_a ? i : first_b + (i - n_a);
-    if (!p.tiles_per_page) {
-      start = t * p.tile_tokens;
-      cnt = p.tile_tokens;
-    } else {
-      const int page = t / p.tiles_per_page, sub = (t - page * p.tiles_per_page) * kTile;
-      start = page * p.c.page_size + sub;
-      cnt = min(kTile, p.c.page_size - sub);
-    }
-  }
   // every token of a tile is attended
   __device__ __forceinline__ bool whole(int start, int cnt) const {
     return start + cnt <= sink || (start >= win0 && start + cnt <= len);
   }
 };
+
+// The attended tiles of a row from the i-th on: first token, tokens, first page and the token's
+// row in it.
+struct Tile {
+  int i, start, cnt, page, sub;
+  __device__ __forceinline__ Tile(const AttParams& p, const Row& row, int i_) : i(i_) {
+    seek(p, i < row.n_a ? i : row.first_b + (i - row.n_a));
+  }
+  __device__ __forceinline__ void seek(const AttParams& p, int t) {
+    if (!p.tiles_per_page) {
+      page = t * p.pages_per_tile;
+      sub = 0;
+      cnt = p.tile_tokens;
+    } else {
+      page = t / p.tiles_per_page;
+      sub = (t - page * p.tiles_per_page) * kTile;
+      cnt = min(kTile, p.c.page_size - sub);
+    }
+    start = page * p.c.page_size + sub;
+  }
+  __device__ __forceinline__ void next(const AttParams& p, const Row& row) {
+    if (++i == row.n_a) {
+      seek(p, row.first_b);
+    } else if (!p.tiles_per_page) {
+      start += cnt;
+      page += p.pages_per_tile;
+    } else {
+      start += cnt;
+      sub += kTile;
+      if (sub >= p.c.page_size) {
+        sub = 0;
+        ++page;
+      }
+      cnt = min(kTile, p.c.page_size - sub);
+    }
+  }
+};
+
+// Stage of a ring and the parity of its current phase, advanced tile by tile.
+template <int kStages>
+struct Ring {
+  int st = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == kStages) {
+      st = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// 64-bit quotient, by the 32-bit division where both fit.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
 
 // A CTA's share of the units, row by row; every role walks it on its own.
 struct Walk {
@@ -288,7 +339,7 @@ struct Walk {
     if (left > 0) {
       row = Row(p, seq_len(p.c, s));
       if (row.count == 0) { left = 0; return; }            // (lengths changed under the call)
-      hc = static_cast<int>(off / row.count);
+      hc = static_cast<int>(quot(off, row.count));
       i0 = static_cast<int>(off - static_cast<long long>(hc) * row.count);
       take();
     }
@@ -318,6 +369,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void sts_bf16(uint32_t addr, float x) {
+  asm volatile("st.shared.b16 [%0], %1;"
+               :: "r"(addr), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x))) : "memory");
+}
+
 // 16 consecutive 32-bit columns of this thread's lane -> registers.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -329,11 +390,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// KFULL / VFULL: a stage has landed.  SDONE: the S product of the tile in K stage i is done (its
+// scores may be read, the stage refilled); ODONE: likewise the O product of V stage i (O holds
+// the tile, P and the stage are free).  SFREE: the scores of a buffer have been read.
 enum Bar {
-  B_KFULL = 0, B_KEMPTY = B_KFULL + kMaxStages, B_VFULL = B_KEMPTY + kMaxStages,
-  B_VEMPTY = B_VFULL + kMaxStages, B_SFULL = B_VEMPTY + kMaxStages, B_SEMPTY = B_SFULL + 2,
-  B_QFULL = B_SEMPTY + 2, B_QEMPTY = B_QFULL + 2, B_PFULL = B_QEMPTY + 2, B_PVDONE, B_FINAL,
-  B_COUNT
+  B_KFULL = 0, B_SDONE = B_KFULL + kMaxStages, B_VFULL = B_SDONE + kMaxStages,
+  B_ODONE = B_VFULL + kMaxStages, B_SFREE = B_ODONE + kMaxStages, B_PFULL = B_SFREE + 2,
+  B_QFULL = B_PFULL + 2, B_QFREE = B_QFULL + 2, B_FINAL = B_QFREE + 2, B_COUNT = B_FINAL + 2
 };
 
 // Bounded wait that ignores the abort flag (used while draining after an abort).
@@ -341,6 +404,70 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t dl = globaltimer() + 100000000ull;
   while (!mbar_try_wait(bar, parity))
     if (globaltimer() > dl) break;
+}
+
+// Units of a call and a CTA's share of them: the first total % G CTAs take one more than the
+// others, and no CTA that takes part is without work.
+struct Share {
+  long long total, each, extra;
+  int G;
+  __device__ __forceinline__ Share(long long total_, int ctas) : total(total_) {
+    G = static_cast<int>(min(static_cast<long long>(ctas), max(total, 1ll)));
+    each = quot(total, G);
+    extra = total - each * G;
+  }
+  __device__ __forceinline__ long long begin(int cta) const {
+    return cta < G ? each * cta + min(static_cast<long long>(cta), extra) : total;
+  }
+  __device__ __forceinline__ int cta_of(long long u) const {
+    const long long split = extra * (each + 1);
+    return static_cast<int>(u < split ? quot(u, each + 1) : extra + quot(u - split, each));
+  }
+};
+
+// The sequence that holds unit `begin(cta)` and the unit's offset in it, by a block-wide scan
+// over the lengths (consecutive sequences per thread).  Two barriers; `warp_s` one word per warp.
+template <int kThreads>
+__device__ __forceinline__ Share find_share(const AttParams& p, int cta, long long* warp_s,
+                                            int* seq_s, long long* off_s) {
+  const int hcs = p.c.Hkv * p.chunks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.c.n_seqs + kThreads - 1) / kThreads;
+  const int sa = min(p.c.n_seqs, static_cast<int>(threadIdx.x) * per);
+  const int se = min(p.c.n_seqs, sa + per);
+  long long mine = 0;
+  for (int s = sa; s < se; ++s) mine += Row(p, seq_len(p.c, s)).count;
+  mine *= hcs;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) warp_s[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_s[w];
+    total += warp_s[w];
+  }
+  const Share sh(total, gridDim.x);
+  const long long u0 = sh.begin(cta);
+  if (u0 >= before && u0 < before + mine) {
+    long long off = u0 - before;
+    for (int s = sa; s < se; ++s) {
+      const long long n = static_cast<long long>(Row(p, seq_len(p.c, s)).count) * hcs;
+      if (off < n) {
+        *seq_s = s;
+        *off_s = off;
+        break;
+      }
+      off -= n;
+    }
+  }
+  __syncthreads();
+  return sh;
 }
 
 template <int D, int N>
@@ -355,9 +482,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
   __shared__ uint32_t tmem_base_s;
   __shared__ AbortState ab;
   __shared__ uint16_t bad_pages[kMetaRing];
-  __shared__ float alpha_s[N], m_s[N], l_s[N];
-  __shared__ long long scan_s[kAttThreads / 32], total_s, off_s;
-  __shared__ int start_s, last_s;
+  __shared__ __align__(16) float m_s[N];           // the heads' running offsets (log2 units)
+  __shared__ __align__(16) float alpha_s[N];       // what a new offset rescales by
+  __shared__ __align__(16) float red_s[4][N];      // per warp: tile maxima, then sums
+  __shared__ long long scan_s[kAttThreads / 32], off_s;
+  __shared__ int start_s;
   __shared__ int loads_s[3];                       // Q, K and V loads sent (for the drain)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(dsmem);
@@ -368,19 +497,17 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(bar(B_KFULL + i), 1);
-      mbar_init(bar(B_KEMPTY + i), 1);
+      mbar_init(bar(B_SDONE + i), 1);
       mbar_init(bar(B_VFULL + i), 1);
-      mbar_init(bar(B_VEMPTY + i), 1);
+      mbar_init(bar(B_ODONE + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(B_SFULL + i), 1);
-      mbar_init(bar(B_SEMPTY + i), 128);
+      mbar_init(bar(B_SFREE + i), 128);
+      mbar_init(bar(B_PFULL + i), 128);
       mbar_init(bar(B_QFULL + i), 1);
-      mbar_init(bar(B_QEMPTY + i), 1);
+      mbar_init(bar(B_QFREE + i), 1);
+      mbar_init(bar(B_FINAL + i), 1);
     }
-    mbar_init(bar(B_PFULL), 128);
-    mbar_init(bar(B_PVDONE), 1);
-    mbar_init(bar(B_FINAL), 1);
     ab.flag = 0;
     start_s = 0;
     off_s = 0;
@@ -392,91 +519,62 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tmem_alloc(smem_u32(&tmem_base_s), SM::kTmemCols);
     tmem_relinquish();
   }
   // columns of P that no head fills must be finite; V rows that no box fills (pages that do not
   // divide a tile) too: P is 0 there, but 0 * NaN is not
-  for (int i = threadIdx.x; i < N * kTile * 2 / 16; i += kAttThreads)
+  for (int i = threadIdx.x; i < 2 * SM::kPBytes / 16; i += kAttThreads)
     reinterpret_cast<uint4*>(gb + SM::kP)[i] = make_uint4(0, 0, 0, 0);
   if (!p.tiles_per_page && p.tile_tokens < kTile)
     for (int i = threadIdx.x; i < SM::kVS * SM::kTileBytes / 16; i += kAttThreads)
       reinterpret_cast<uint4*>(gb + SM::kV)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  // units before each sequence: a block-wide scan, `per` consecutive sequences per thread
-  const int hcs = p.c.Hkv * p.chunks;
-  const int per = (p.c.n_seqs + kAttThreads - 1) / kAttThreads;
-  const int sa = min(p.c.n_seqs, static_cast<int>(threadIdx.x) * per);
-  const int se = min(p.c.n_seqs, sa + per);
-  long long mine = 0;
-  for (int s = sa; s < se; ++s) mine += static_cast<long long>(Row(p, seq_len(p.c, s)).count) * hcs;
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) scan_s[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kAttThreads / 32; ++w) {
-    if (w < warp) before += scan_s[w];
-    total += scan_s[w];
-  }
-  // CTAs that have work: no more than units, so that each of them has at least one
-  const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1ll)));
-  const int cta = blockIdx.x;
-  const long long u0 = cta < G ? total * cta / G : total;
-  const long long u1 = cta < G ? total * (cta + 1) / G : total;
-  if (u0 >= before && u0 < before + mine) {        // this thread's sequences hold the first unit
-    long long off = u0 - before;
-    for (int s = sa; s < se; ++s) {
-      const long long n = static_cast<long long>(Row(p, seq_len(p.c, s)).count) * hcs;
-      if (off < n) {
-        start_s = s;
-        off_s = off;
-        break;
-      }
-      off -= n;
-    }
-  }
   tc_fence_before();
-  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int cta = blockIdx.x;
+  const Share sh = find_share<kAttThreads>(p, cta, scan_s, &start_s, &off_s);
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   const uint64_t deadline = globaltimer() + p.timeout_ns;
-  Walk w(p, start_s, off_s, u1 - u0);
+  const long long u1 = sh.begin(cta + 1);
+  Walk w(p, start_s, off_s, u1 - sh.begin(cta));
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------- TMA producer
-    // K(j), then V(j - 1): the order in which the MMA warp takes them.  Lane i loads page i of
+    // K(j), then V(j - 1): the order in which the products take them.  Lane i loads page i of
     // the tile; pages without an attended token are left alone (their rows are masked).
     int j = 0, seg = 0;
+    Ring<SM::kKS> rk;
+    Ring<SM::kVS> rv;
     bool ok = true;
     int v_c2 = -1, v_row = 0, v_np = 0;            // the previous tile's boxes
     auto load = [&](int full, uint32_t dst, const CUtensorMap* tm, int c2, int row, int np) {
       if (lane == 0) mbar_arrive_expect_tx(bar(full), np * p.box_rows * D * 2);
       __syncwarp();
-      if (c2 >= 0)
+      if (c2 < 0) return;
+      if (p.one_box) {
+        tma_load_5d(dst + lane * p.box_rows * D * 2, tm, bar(full), 0, 0, 0, row >> 3, c2);
+      } else {                                     // a large page whose rows end inside a group
         for (int pp = 0; pp < D / 64; ++pp)
-          tma_load_3d(dst + pp * (kTile * 128) + (p.tiles_per_page ? 0 : lane * p.box_rows * 128),
-                      tm, bar(full), pp * 64, row, c2);
+          tma_load_3d(dst + pp * (kTile * 128), tm, bar(full), pp * 64, row, c2);
+      }
     };
     auto load_v = [&](int jv) {
-      const int st = jv % SM::kVS;
       if (jv >= SM::kVS)
-        ok = mbar_wait(bar(B_VEMPTY + st), (jv / SM::kVS - 1) & 1, &ab, deadline, p.c.status);
+        ok = mbar_wait(bar(B_ODONE + rv.st), rv.parity ^ 1, &ab, deadline, p.c.status);
       if (!__all_sync(~0u, ok)) { ok = false; return; }
-      load(B_VFULL + st, sb + SM::kV + st * SM::kTileBytes, &tm_v, v_c2, v_row, v_np);
+      load(B_VFULL + rv.st, sb + SM::kV + rv.st * SM::kTileBytes, &tm_v, v_c2, v_row, v_np);
       if (lane == 0) loads_s[2] = jv + 1;
+      rv.next();
     };
     for (; ok && w.left > 0; w.next(p), ++seg) {
       const int* table = p.c.table + static_cast<long long>(w.s) * p.c.max_pages;
       const int kvh = w.hc / p.chunks, chunk = w.hc - kvh * p.chunks;
       if (seg >= 2)
-        ok = mbar_wait(bar(B_QEMPTY + (seg & 1)), ((seg >> 1) - 1) & 1, &ab, deadline, p.c.status);
+        ok = mbar_wait(bar(B_QFREE + (seg & 1)), ((seg >> 1) - 1) & 1, &ab, deadline, p.c.status);
       if (!__all_sync(~0u, ok)) { ok = false; break; }
       if (lane == 0) {
         mbar_arrive_expect_tx(bar(B_QFULL + (seg & 1)), N * D * 2);
@@ -485,13 +583,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
                       bar(B_QFULL + (seg & 1)), pp * 64, chunk * N, w.s * p.c.Hkv + kvh);
         loads_s[0] = seg + 1;
       }
-      for (int i = 0; ok && i < w.n; ++i, ++j) {
-        int start, cnt;
-        w.row.tile(p, w.i0 + i, start, cnt);
+      Tile tile(p, w.row, w.i0);
+      for (int i = 0; ok && i < w.n; ++i, ++j, tile.next(p, w.row)) {
         // this lane's page
-        const int first = p.tiles_per_page ? start : start + lane * p.c.page_size;
-        const int page_no = start / p.c.page_size + (p.tiles_per_page ? 0 : lane);
-        bool need = p.tiles_per_page ? lane == 0 : lane * p.c.page_size < cnt;
+        const int page_no = tile.page + lane;
+        const int first = tile.start + lane * p.c.page_size;
+        bool need = lane < p.pages_per_tile;
         need = need && (first < w.row.sink ||
                         (first + p.c.page_size > w.row.win0 && first < w.row.len));
         int c2 = -1;
@@ -505,14 +602,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
         const uint32_t bad_mask = __ballot_sync(~0u, bad);
         if (bad_mask && lane == 0) atomicOr(p.c.status, kStatusPage);
         const int np = __popc(__ballot_sync(~0u, need));
-        const int row = p.tiles_per_page ? start - page_no * p.c.page_size : 0;
-        const int st = j % SM::kKS;
+        const int row = tile.sub;
         if (j >= SM::kKS)
-          ok = mbar_wait(bar(B_KEMPTY + st), (j / SM::kKS - 1) & 1, &ab, deadline, p.c.status);
+          ok = mbar_wait(bar(B_SDONE + rk.st), rk.parity ^ 1, &ab, deadline, p.c.status);
         if (!__all_sync(~0u, ok)) { ok = false; break; }
         if (lane == 0) bad_pages[j & (kMetaRing - 1)] = static_cast<uint16_t>(bad_mask);
-        load(B_KFULL + st, sb + SM::kK + st * SM::kTileBytes, &tm_k, c2, row, np);
+        load(B_KFULL + rk.st, sb + SM::kK + rk.st * SM::kTileBytes, &tm_k, c2, row, np);
         if (lane == 0) loads_s[1] = j + 1;
+        rk.next();
         if (j > 0) load_v(j - 1);
         v_c2 = c2;
         v_row = row;
@@ -520,58 +617,68 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       }
     }
     if (ok && j > 0) load_v(j - 1);
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------- MMA issuer
+  } else if (warp == kScoreWarp) {
+    // ------------------------------------------------------------------- S = K Q^T
     if (lane == 0) {
       int j = 0, seg = 0;
-      bool ok = true, prev_first = false;
-      auto pv = [&](int jv, bool first_of_segment) -> bool {
-        const int st = jv % SM::kVS;
-        if (!mbar_wait(bar(B_VFULL + st), (jv / SM::kVS) & 1, &ab, deadline, p.c.status) ||
-            !mbar_wait(bar(B_PFULL), jv & 1, &ab, deadline, p.c.status))
-          return false;
-        tc_fence_after();
-        const uint64_t a = sdesc_sw128(sb + SM::kV + st * SM::kTileBytes, kTile * 128, 1024);
-        const uint64_t b = sdesc_sw128(sb + SM::kP, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ss(tmem + SM::kColO, a + kk * 128, b + (kk >> 2) * (N * 8) + (kk & 3) * 2,
-                  SM::kIdescO, !(first_of_segment && kk == 0));
-        umma_commit(bar(B_VEMPTY + st));
-        umma_commit(bar(B_PVDONE));
-        return true;
-      };
+      Ring<SM::kKS> rk;
+      bool ok = true;
+      const uint32_t panel = static_cast<uint32_t>(p.panel_bytes) >> 4;    // descriptor units
       for (; ok && w.left > 0; w.next(p), ++seg) {
         ok = mbar_wait(bar(B_QFULL + (seg & 1)), (seg >> 1) & 1, &ab, deadline, p.c.status);
         const uint64_t b = sdesc_sw128(sb + SM::kQ + (seg & 1) * N * D * 2, 16, 1024);
-        for (int i = 0; ok && i < w.n; ++i, ++j) {
-          const int st = j % SM::kKS, sbuf = j & 1;
-          ok = mbar_wait(bar(B_KFULL + st), (j / SM::kKS) & 1, &ab, deadline, p.c.status) &&
-               (j < 2 || mbar_wait(bar(B_SEMPTY + sbuf), ((j >> 1) - 1) & 1, &ab, deadline,
-                                   p.c.status));
+        for (int i = 0; ok && i < w.n; ++i, ++j, rk.next()) {
+          const int st = rk.st, sbuf = j & 1;
+          ok = (j < 2 || mbar_wait(bar(B_SFREE + sbuf), ((j >> 1) - 1) & 1, &ab, deadline,
+                                   p.c.status)) &&
+               mbar_wait(bar(B_KFULL + st), rk.parity, &ab, deadline, p.c.status);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t a = sdesc_sw128(sb + SM::kK + st * SM::kTileBytes, 16, 1024);
+          const uint64_t a = sdesc_sw128(sb + SM::kK + st * SM::kTileBytes, 16, p.group_bytes);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(tmem + sbuf * N, a + (kk >> 2) * 1024 + (kk & 3) * 2,
+            umma_ss(tmem + sbuf * N, a + (kk >> 2) * panel + (kk & 3) * 2,
                     b + (kk >> 2) * (N * 8) + (kk & 3) * 2, SM::kIdescS, kk != 0);
-          umma_commit(bar(B_SFULL + sbuf));
-          umma_commit(bar(B_KEMPTY + st));
-          if (i + 1 == w.n) umma_commit(bar(B_QEMPTY + (seg & 1)));
-          if (j > 0) ok = pv(j - 1, prev_first);
-          prev_first = i == 0;
+          umma_commit(bar(B_SDONE + st));
+          if (i + 1 == w.n) umma_commit(bar(B_QFREE + (seg & 1)));
         }
       }
-      if (ok && j > 0) pv(j - 1, prev_first);
+    }
+    __syncwarp();
+  } else if (warp == kOutWarp) {
+    // ------------------------------------------------------------------- O += V^T P^T
+    if (lane == 0) {
+      int j = 0;
+      Ring<SM::kVS> rv;
+      bool ok = true;
+      const uint32_t keys16 = static_cast<uint32_t>(p.group_bytes) >> 3;   // two row groups
+      for (; ok && w.left > 0; w.next(p)) {
+        for (int i = 0; i < w.n; ++i, ++j, rv.next()) {
+          const int st = rv.st;
+          ok = mbar_wait(bar(B_VFULL + st), rv.parity, &ab, deadline, p.c.status) &&
+               mbar_wait(bar(B_PFULL + (j & 1)), (j >> 1) & 1, &ab, deadline, p.c.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = sdesc_sw128(sb + SM::kV + st * SM::kTileBytes, p.panel_bytes,
+                                         p.group_bytes);
+          const uint64_t b = sdesc_sw128(sb + SM::kP + (j & 1) * SM::kPBytes, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ss(tmem + SM::kColO, a + kk * keys16, b + (kk >> 2) * (N * 8) + (kk & 3) * 2,
+                    SM::kIdescO, !(i == 0 && kk == 0));
+          umma_commit(bar(B_ODONE + st));
+        }
+      }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------- softmax (warps 0-3)
     const int t = threadIdx.x;                     // key row = TMEM lane; O^T: element of d
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    float* sc = reinterpret_cast<float*>(gb + SM::kS);
-    constexpr int HW = N / 4;                      // heads of a warp: warp, warp + 4, ...
+    constexpr int CH = N < 32 ? 16 : 32;           // columns of one TMEM access
+    auto ld_cols = [&](uint32_t at, uint32_t (&r)[CH]) {
+      if constexpr (CH == 16) tmem_ld16(at, r); else tmem_ld32(at, r);
+    };
     // sequences with nothing to attend
     for (int s = cta; s < p.c.n_seqs; s += gridDim.x) {
       if (Row(p, seq_len(p.c, s)).count) continue;
@@ -581,198 +688,195 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
         for (int i = t; i < p.c.H; i += 128)
           p.lse[static_cast<long long>(s) * p.c.H + i] = -INFINITY;
     }
+    // this key's place in P: row g (head), column t, 128-byte swizzle
+    const uint32_t p_col0 = sb + SM::kP + (t >> 6) * (N * 128) + (t & 7) * 2;
+    const int chunk16 = (t & 63) >> 3;
     int j = 0;
+    Ring<SM::kKS> rk;
+    Ring<SM::kVS> rv, rv1, rv2;                    // V stages of tiles j, j - 1, j - 2
     bool ok = true;
+    auto o_done = [&](const Ring<SM::kVS>& r) {    // the O product of the tile is complete
+      return mbar_wait(bar(B_ODONE + r.st), r.parity, &ab, deadline, p.c.status);
+    };
     for (; ok && w.left > 0; w.next(p)) {
       const int kvh = w.hc / p.chunks, chunk = w.hc - kvh * p.chunks;
       const int nh = min(N, p.group - chunk * N);  // heads of this chunk
-      float m[HW], l[HW];
+      float l[N];                                  // this key's share of the heads' sums
 #pragma unroll
-      for (int i = 0; i < HW; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-      }
-      for (int i = 0; i < w.n; ++i, ++j) {
-        int start, cnt;
-        w.row.tile(p, w.i0 + i, start, cnt);
-        ok = mbar_wait(bar(B_SFULL + (j & 1)), (j >> 1) & 1, &ab, deadline, p.c.status);
-        if (!named_bar_and(1, 128, ok)) { ok = false; break; }
+      for (int g = 0; g < N; ++g) l[g] = 0.f;
+      Tile tile(p, w.row, w.i0);
+      for (int i = 0; i < w.n; ++i, ++j, tile.next(p, w.row)) {
+        const bool whole = w.row.whole(tile.start, tile.cnt);
+        bool live = t < tile.cnt && (whole || w.row.attended(tile.start + t));
+        ok = ok && mbar_wait(bar(B_SDONE + rk.st), rk.parity, &ab, deadline, p.c.status);
+        rk.next();
+        __syncwarp();
         tc_fence_after();
         uint32_t s[N];
-        if constexpr (N == 16) {
-          tmem_ld16(tmem + lane_off + (j & 1) * N, *reinterpret_cast<uint32_t(*)[16]>(&s[0]));
-        } else {
 #pragma unroll
-          for (int c = 0; c < N; c += 32)
-            tmem_ld32(tmem + lane_off + (j & 1) * N + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
-        }
+        for (int c = 0; c < N; c += CH)
+          ld_cols(tmem + lane_off + (j & 1) * N + c, *reinterpret_cast<uint32_t(*)[CH]>(&s[c]));
+        const uint32_t bad = bad_pages[j & (kMetaRing - 1)];
+        if (bad) live = live && !((bad >> (p.tiles_per_page ? 0 : t / p.c.page_size)) & 1u);
         tmem_wait_ld();
         tc_fence_before();
-        mbar_arrive(bar(B_SEMPTY + (j & 1)));
-        const uint32_t bad = bad_pages[j & (kMetaRing - 1)];
-        bool live = t < cnt && w.row.attended(start + t);
-        if (bad) live = live && !((bad >> (p.tiles_per_page ? 0 : t / p.c.page_size)) & 1u);
+        mbar_arrive(bar(B_SFREE + (j & 1)));
+        // scores in log2 units relative to the running offsets: does any exceed them by > 2^8?
+        // (Heads are taken four at a time; those past nh have zero queries and offset 0.)
+        float z[N];
+        bool over = i == 0;
+        if (i > 0) {
+          float top = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < N; ++g)
-          if (g < nh) sc[g * kTile + t] = live ? __uint_as_float(s[g]) : -INFINITY;
-        named_bar_sync(1, 128);
-        bool grown = false;
-        uint2 pk[HW];
+          for (int g = 0; g < N; g += 4) {
+            if (g >= nh) break;
+            const float4 m4 = *reinterpret_cast<const float4*>(&m_s[g]);
+            const float m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
-        for (int k = 0; k < HW; ++k) {
-          const int g = warp + 4 * k;
-          if (g >= nh) break;
-          const float4 x = *reinterpret_cast<const float4*>(sc + g * kTile + 4 * lane);
-          float mt = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
-#pragma unroll
-          for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, o));
-          mt *= p.scale_log2;
-          float alpha = 1.f;
-          if (mt > m[k] + kRescale || m[k] == -INFINITY) {   // -inf: nothing attended so far
-            if (m[k] > -INFINITY) {
-              alpha = ex2(m[k] - mt);
-              grown = true;
+            for (int e = 0; e < 4; ++e) {
+              z[g + e] = fmaf(__uint_as_float(s[g + e]), p.scale_log2, -m[e]);
+              top = fmaxf(top, z[g + e]);
             }
-            m[k] = mt;
           }
-          const float me = m[k] > -INFINITY ? m[k] : 0.f;
-          const float4 e = make_float4(
-              ex2(fmaf(x.x, p.scale_log2, -me)), ex2(fmaf(x.y, p.scale_log2, -me)),
-              ex2(fmaf(x.z, p.scale_log2, -me)), ex2(fmaf(x.w, p.scale_log2, -me)));
-          l[k] = l[k] * alpha + ((e.x + e.y) + (e.z + e.w));
-          pk[k] = make_uint2(pack2(e.x, e.y), pack2(e.z, e.w));
-          if (lane == 0) alpha_s[g] = alpha;
+          over = live && top > kRescale;
         }
-        // P(j - 1) V(j - 1) is done: P may be overwritten, O rescaled
-        if (j > 0) ok = mbar_wait(bar(B_PVDONE), (j - 1) & 1, &ab, deadline, p.c.status);
+        if (!named_bar_and(1, 128, ok && !over)) {
+          // new offsets: the tile's maxima where they exceed the old ones by more than 2^8
+          if (!named_bar_and(1, 128, ok)) { ok = false; break; }
 #pragma unroll
-        for (int k = 0; k < HW; ++k) {
-          const int g = warp + 4 * k;
+          for (int g = 0; g < N; g += 4) {
+            if (g >= nh) break;
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = warp_max(live ? __uint_as_float(s[g + e]) : -INFINITY);
+            if (lane == 0)
+              *reinterpret_cast<float4*>(&red_s[warp][g]) = make_float4(x[0], x[1], x[2], x[3]);
+          }
+          if (j > 0) ok = o_done(rv1);             // O may be rescaled
+          named_bar_sync(1, 128);
+          if (t < N) {
+            float m = 0.f, alpha = 1.f;
+            if (t < nh) {
+              const float mt = fmaxf(fmaxf(red_s[0][t], red_s[1][t]),
+                                     fmaxf(red_s[2][t], red_s[3][t])) * p.scale_log2;
+              m = i > 0 ? m_s[t] : -INFINITY;
+              if (m == -INFINITY || mt > m + kRescale) {
+                if (m > -INFINITY) alpha = ex2(m - mt);
+                m = mt;
+              }
+            }
+            m_s[t] = m;
+            alpha_s[t] = alpha;
+          }
+          named_bar_sync(1, 128);
+          if (i > 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < N; c += CH) {
+              if (c >= nh) break;
+              uint32_t o[CH];
+              ld_cols(tmem + lane_off + SM::kColO + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < CH; e += 4) {
+                const float4 a4 = *reinterpret_cast<const float4*>(&alpha_s[c + e]);
+                const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                  l[c + e + f] *= a[f];
+                  o[e + f] = __float_as_uint(__uint_as_float(o[e + f]) * a[f]);
+                }
+              }
+              if constexpr (CH == 16) tmem_st16(tmem + lane_off + SM::kColO + c, o);
+              else tmem_st32(tmem + lane_off + SM::kColO + c, o);
+            }
+            tmem_wait_st();
+          }
+#pragma unroll
+          for (int g = 0; g < N; g += 4) {
+            if (g >= nh) break;
+            const float4 m4 = *reinterpret_cast<const float4*>(&m_s[g]);
+            const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+            // an offset of -inf: every score so far is -inf as well, and weighs nothing
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              z[g + e] = fmaf(__uint_as_float(s[g + e]), p.scale_log2,
+                              m[e] > -INFINITY ? -m[e] : 0.f);
+          }
+        } else if (j > 1) {
+          ok = o_done(rv2);                        // its P buffer may be overwritten
+        }
+        rv2 = rv1;
+        rv1 = rv;
+        const uint32_t p_col = p_col0 + (j & 1) * SM::kPBytes;
+#pragma unroll
+        for (int g = 0; g < N; g += 4) {
           if (g >= nh) break;
-          const int byte = (8 * lane) & 127;
-          *reinterpret_cast<uint2*>(gb + SM::kP + (lane >> 4) * (N * 128) + g * 128 +
-                                    (((byte >> 4) ^ (g & 7)) << 4) + (byte & 15)) = pk[k];
-        }
-        if (!w.row.whole(start, cnt)) {
-          // rows without an attended token may hold anything
-          ok = ok && mbar_wait(bar(B_VFULL + j % SM::kVS), (j / SM::kVS) & 1, &ab, deadline,
-                               p.c.status);
-          if (!live && t < cnt)
-            for (int c = 0; c < D / 8; ++c)
-              *reinterpret_cast<uint4*>(gb + SM::kV + (j % SM::kVS) * SM::kTileBytes +
-                                        (c >> 3) * (kTile * 128) + t * 128 + ((c & 7) << 4)) =
-                  make_uint4(0, 0, 0, 0);
-        }
-        const bool same = named_bar_and(1, 128, !grown);
-        if (!same && i > 0) {
-          tc_fence_after();
-          constexpr int CH = N < 32 ? 16 : 32;
-#pragma unroll 1
-          for (int c = 0; c < N; c += CH) {
-            uint32_t o[CH];
-            const uint32_t at = tmem + lane_off + SM::kColO + c;
-            if constexpr (CH == 16) tmem_ld16(at, o); else tmem_ld32(at, o);
-            tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < CH; ++e)
-              if (c + e < nh) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_s[c + e]);
-            if constexpr (CH == 16) tmem_st16(at, o); else tmem_st32(at, o);
+          for (int e = 0; e < 4; ++e) {
+            const float x = live ? ex2(z[g + e]) : 0.f;
+            l[g + e] += x;
+            sts_bf16(p_col + (g + e) * 128 + ((chunk16 ^ ((g + e) & 7)) << 4), x);
           }
-          tmem_wait_st();
         }
+        if (!whole) {
+          // rows without an attended token may hold anything
+          ok = ok && mbar_wait(bar(B_VFULL + rv.st), rv.parity, &ab, deadline, p.c.status);
+          if (!live && t < tile.cnt)
+            for (int c = 0; c < D / 8; ++c)
+              *reinterpret_cast<uint4*>(gb + SM::kV + rv.st * SM::kTileBytes +
+                                        (t >> 3) * p.group_bytes + (c >> 3) * p.panel_bytes +
+                                        (t & 7) * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+        }
+        rv.next();
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(bar(B_PFULL));
+        mbar_arrive(bar(B_PFULL + (j & 1)));
       }
       // the row's result, or this CTA's part of it
-      if (ok) ok = mbar_wait(bar(B_PVDONE), (j - 1) & 1, &ab, deadline, p.c.status);
+      if (ok) ok = o_done(rv1);
       if (!named_bar_and(1, 128, ok)) { ok = false; break; }
       tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < HW; ++k) {
-        const int g = warp + 4 * k;
-        if (g >= nh) break;
-        float x = l[k];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-        if (lane == 0) {
-          m_s[g] = m[k];
-          l_s[g] = x;
-        }
-      }
       uint32_t o[N];
-      if constexpr (N == 16) {
-        tmem_ld16(tmem + lane_off + SM::kColO, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-      } else {
 #pragma unroll
-        for (int c = 0; c < N; c += 32)
-          tmem_ld32(tmem + lane_off + SM::kColO + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c]));
+      for (int c = 0; c < N; c += CH)
+        ld_cols(tmem + lane_off + SM::kColO + c, *reinterpret_cast<uint32_t(*)[CH]>(&o[c]));
+#pragma unroll
+      for (int g = 0; g < N; g += 4) {
+        if (g >= nh) break;
+        float x[4] = {l[g], l[g + 1], l[g + 2], l[g + 3]};
+#pragma unroll
+        for (int k = 16; k; k >>= 1)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] += __shfl_xor_sync(~0u, x[e], k);
+        if (lane == 0)
+          *reinterpret_cast<float4*>(&red_s[warp][g]) = make_float4(x[0], x[1], x[2], x[3]);
       }
       tmem_wait_ld();
       tc_fence_before();
       named_bar_sync(1, 128);
       const long long head0 = static_cast<long long>(w.s) * p.c.H + kvh * p.group + chunk * N;
-      if (w.n == w.row.count) {
-        if (t < D) {
-#pragma unroll
-          for (int g = 0; g < N; ++g)
-            if (g < nh)
-              p.out[(head0 + g) * D + t] = __float2bfloat16_rn(
-                  l_s[g] > 0.f ? __uint_as_float(o[g]) / l_s[g] : 0.f);
-        }
-        if (p.lse && t < nh)
-          p.lse[head0 + t] =
-              l_s[t] > 0.f ? (m_s[t] + log2f(l_s[t])) * 0.69314718055994530942f : -INFINITY;
-        continue;
-      }
       const long long slot = (static_cast<long long>(cta) * 2 + (w.first ? 0 : 1)) * N;
+      const bool complete = w.n == w.row.count;
+      if (t < nh) {
+        const float lg = (red_s[0][t] + red_s[1][t]) + (red_s[2][t] + red_s[3][t]);
+        if (!complete)
+          p.part_ml[slot + t] = make_float2(m_s[t], lg);
+        else if (p.lse)
+          p.lse[head0 + t] = lg == 0.f ? -INFINITY : (m_s[t] + log2f(lg)) * 0.69314718055994530942f;
+      }
       if (t < D) {
 #pragma unroll
-        for (int g = 0; g < N; ++g)
-          if (g < nh) p.part_o[(slot + g) * D + t] = __uint_as_float(o[g]);
-      }
-      if (t < nh) p.part_ml[slot + t] = make_float2(m_s[t], l_s[t]);
-      __threadfence();
-      // the CTAs of this row: units [a, a + count); its counter is the last one's, for which no
-      // other shared row can be the one that started before it
-      const long long a = u1 - w.left - w.i0;
-      const int c0 = static_cast<int>(((a + 1) * G - 1) / total);
-      const int c1 = static_cast<int>(((a + w.row.count) * G - 1) / total);
-      named_bar_sync(1, 128);
-      if (t == 0) last_s = atomicAdd(&p.part_cnt[c1], 1) == c1 - c0;
-      named_bar_sync(1, 128);
-      if (!last_s) continue;
-      __threadfence();
-      // M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L, in CTA order
-      const bool aligned = total * c0 / G == a;    // the row's first CTA starts with it
-      for (int g = 0; g < nh; ++g) {
-        auto part = [&](int c) {
-          return (static_cast<long long>(c) * 2 + (c > c0 || aligned ? 0 : 1)) * N + g;
-        };
-        float M = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(&p.part_ml[part(c)]).x);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
-        float L = 0.f, acc = 0.f;
-        for (int cb = c0; cb <= c1; cb += 32) {
-          float wt = 0.f;
-          if (cb + lane <= c1) {
-            const float2 ml = __ldcg(&p.part_ml[part(cb + lane)]);
-            wt = ml.x > -INFINITY ? ex2(ml.x - M) : 0.f;
-            L += wt * ml.y;
-          }
-          const int n = min(32, c1 - cb + 1);
-#pragma unroll 4
-          for (int c = 0; c < n; ++c) {
-            const float wc = __shfl_sync(~0u, wt, c);
-            if (t < D) acc += wc * __ldcg(&p.part_o[part(cb + c) * D + t]);
+        for (int g = 0; g < N; ++g) {
+          if (g >= nh) break;
+          const float og = __uint_as_float(o[g]);
+          if (complete) {
+            const float lg = (red_s[0][g] + red_s[1][g]) + (red_s[2][g] + red_s[3][g]);
+            p.out[(head0 + g) * D + t] = __float2bfloat16_rn(lg == 0.f ? 0.f : __fdividef(og, lg));
+          } else {
+            p.part_o[(slot + g) * D + t] = og;
           }
         }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
-        if (t < D) p.out[(head0 + g) * D + t] = __float2bfloat16_rn(L > 0.f ? acc / L : 0.f);
-        if (p.lse && t == 0)
-          p.lse[head0 + g] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
       }
     }
   }
@@ -781,9 +885,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
   __syncthreads();
   if (ab.flag) {
     // something gave up: the copies and MMAs in flight end before their memory is released
-    if (warp == kMmaWarp && lane == 0) {
-      umma_commit(bar(B_FINAL));
-      drain_wait(bar(B_FINAL), 0);
+    if ((warp == kScoreWarp || warp == kOutWarp) && lane == 0) {
+      umma_commit(bar(B_FINAL + (warp == kOutWarp)));
+      drain_wait(bar(B_FINAL + (warp == kOutWarp)), 0);
+    }
+    if (warp == kProducerWarp && lane == 0) {
       for (int i = max(0, loads_s[0] - 2); i < loads_s[0]; ++i)
         drain_wait(bar(B_QFULL + (i & 1)), (i >> 1) & 1);
       for (int i = max(0, loads_s[1] - SM::kKS); i < loads_s[1]; ++i)
@@ -794,9 +900,73 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
     tc_fence_before();
     __syncthreads();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, SM::kTmemCols);
+  }
+}
+
+// Block b joins the row that ends in CTA b's share and began in an earlier one's, if there is
+// one:  M = max m,  L = sum l 2^(m - M),  O = sum O 2^(m - M) / L  over its CTAs, in order.  The
+// row is found while the attention kernel still runs.  One head per pass, an element of d per
+// thread.
+constexpr int kJoinThreads = 128;
+
+template <int D, int N>
+__global__ void __launch_bounds__(kJoinThreads)
+paged_join_kernel(const __grid_constant__ AttParams p) {
+  __shared__ long long scan_s[kJoinThreads / 32], off_s;
+  __shared__ int seq_s;
+  if (threadIdx.x == 0) {
+    seq_s = 0;
+    off_s = 0;
+  }
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.x;
+  // (the lengths were there before the attention kernel began)
+  const Share sh = find_share<kJoinThreads>(p, b, scan_s, &seq_s, &off_s);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (b == 0 || b >= sh.G) return;
+  const int s = seq_s;
+  const Row row(p, seq_len(p.c, s));
+  if (row.count == 0) return;
+  const long long u0 = sh.begin(b), u1 = sh.begin(b + 1);
+  const int hc = static_cast<int>(quot(off_s, row.count));
+  const long long a = u0 - (off_s - static_cast<long long>(hc) * row.count);   // the row's units
+  if (a == u0 || a + row.count > u1) return;
+  const int c0 = sh.cta_of(a), n = b - c0 + 1;
+  const bool aligned = sh.begin(c0) == a;          // c0's share starts with the row
+  const int kvh = hc / p.chunks, chunk = hc - kvh * p.chunks;
+  const int nh = min(N, p.group - chunk * N);
+  const long long head0 = static_cast<long long>(s) * p.c.H + kvh * p.group + chunk * N;
+  const int sub = threadIdx.x / D, e = threadIdx.x % D;      // D = 64: two heads per pass
+  for (int g = sub; g < nh; g += kJoinThreads / D) {
+    auto part = [&](int i) {
+      return (static_cast<long long>(c0 + i) * 2 + (i > 0 || aligned ? 0 : 1)) * N + g;
+    };
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&p.part_ml[part(i)]).x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+    float L = 0.f, acc = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float wt = 0.f;
+      if (i0 + lane < n) {
+        const float2 ml = __ldcg(&p.part_ml[part(i0 + lane)]);
+        wt = ml.x > -INFINITY ? ex2(ml.x - M) : 0.f;
+        L += wt * ml.y;
+      }
+      const int k = min(32, n - i0);
+#pragma unroll 8
+      for (int i = 0; i < k; ++i)
+        acc += __shfl_sync(~0u, wt, i) * __ldcg(&p.part_o[part(i0 + i) * D + e]);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+    p.out[(head0 + g) * D + e] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+    if (p.lse && e == 0)
+      p.lse[head0 + g] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
   }
 }
 
@@ -885,7 +1055,7 @@ static void launch_append(const AppendParams& p, cudaStream_t st) {
 // scratch of an attention call.
 struct AttPlan {
   int N, grid;
-  size_t ml, o, total;                     // byte offsets behind the counters; all 256-aligned
+  size_t o, total;                         // byte offset of the partial O behind m and l
 };
 
 static AttPlan att_plan(const Cache& c, int D) {
@@ -898,8 +1068,7 @@ static AttPlan att_plan(const Cache& c, int D) {
   a.grid = n_sm;
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const size_t parts = static_cast<size_t>(a.grid) * 2 * a.N;
-  a.ml = up(a.grid * sizeof(int));
-  a.o = a.ml + up(parts * sizeof(float2));
+  a.o = up(parts * sizeof(float2));
   a.total = a.o + up(parts * D * sizeof(float));
   return a;
 }
@@ -922,8 +1091,9 @@ static int launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const 
       return check_launch("prsink_paged_attention");
     if (dev >= 0 && dev < 64) allowed[dev] = true;
   }
-  paged_attention_kernel<D, N><<<grid, kAttThreads, smem, st>>>(mq, mk, mv, p);
-  count_launch();
+  launch_dependent(paged_attention_kernel<D, N>, grid, kAttThreads, smem, st, mq, mk, mv, p);
+  launch_dependent(paged_join_kernel<D, N>, grid, kJoinThreads, 0, st, p);
+  count_launch(2);
   return check_launch("prsink_paged_attention");
 }
 
@@ -1047,26 +1217,31 @@ extern "C" int prsink_paged_attention(const prsink_paged* paged, const void* q,
   p.chunks = (p.group + pl.N - 1) / pl.N;
   const int ps = p.c.page_size;
   p.tiles_per_page = ps < kTile ? 0 : (ps + kTile - 1) / kTile;
-  p.tile_tokens = ps < kTile ? kTile / ps * ps : kTile;
+  p.pages_per_tile = ps < kTile ? kTile / ps : 1;
+  p.tile_tokens = ps < kTile ? p.pages_per_tile * ps : kTile;
   p.box_rows = ps < kTile ? ps : kTile;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.timeout_ns = 2000000000ull;
   char* base = static_cast<char*>(scratch);
-  p.part_cnt = reinterpret_cast<int*>(base);
-  p.part_ml = reinterpret_cast<float2*>(base + pl.ml);
+  p.part_ml = reinterpret_cast<float2*>(base);
   p.part_o = reinterpret_cast<float*>(base + pl.o);
   CUtensorMap mq, mk, mv;
   const uint64_t rows = static_cast<uint64_t>(p.c.n_pages) * p.c.Hkv;
   rc = make_map(&mq, q, D, p.group, static_cast<uint64_t>(p.c.n_seqs) * p.c.Hkv, 2ull * D,
                 2ull * D * p.group, pl.N, 1);
-  if (!rc) rc = make_map(&mk, k_pages, D, ps, rows, 2ull * D, 2ull * D * ps, p.box_rows, 1);
-  if (!rc) rc = make_map(&mv, v_pages, D, ps, rows, 2ull * D, 2ull * D * ps, p.box_rows, 1);
+  p.one_box = ps % 8 == 0;
+  p.group_bytes = p.one_box ? D / 64 * 1024 : 1024;
+  p.panel_bytes = p.one_box && D > 64 ? 1024 : kTile * 128;
+  auto map = [&](CUtensorMap* m, const void* pages) {
+    return p.one_box ? make_map_rows(m, pages, D, ps, rows, p.box_rows / 8)
+                     : make_map(m, pages, D, ps, rows, 2ull * D, 2ull * D * ps, p.box_rows, 1);
+  };
+  if (!rc) rc = map(&mk, k_pages);
+  if (!rc) rc = map(&mv, v_pages);
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(p.part_cnt, 0, pl.grid * sizeof(int), st) != cudaSuccess)
-    return check_launch(what);
   auto go = [&](auto tag) { return launch_attention<decltype(tag)::d, decltype(tag)::n>(
       mq, mk, mv, p, pl.grid, st); };
   if (D == 128)

@@ -76,26 +76,41 @@ static EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 3-D bf16 tensor map with a 64 x box1 x box2 box and 128-byte swizzle.
-int make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-             uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box1, uint32_t box2) {
+static int encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                      const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) {
     set_error("cuTensorMapEncodeTiled is not available from the driver");
     return PRSINK_ERR_LAUNCH;
   }
-  const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
-  const cuuint32_t box[3] = {64, box1, box2};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     set_error("cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
     return PRSINK_ERR_LAUNCH;
   }
   return PRSINK_OK;
+}
+
+// 3-D bf16 tensor map with a 64 x box1 x box2 box and 128-byte swizzle.
+int make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+             uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box1, uint32_t box2) {
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
+  const cuuint32_t box[3] = {64, box1, box2};
+  return encode_map(m, base, 3, dims, strides, box);
+}
+
+int make_map_rows(CUtensorMap* m, const void* base, int D, uint64_t rows, uint64_t n_blocks,
+                  uint32_t box_groups) {
+  const cuuint64_t row = 2ull * D;
+  const cuuint32_t panels = D / 64;
+  const cuuint64_t dims[5] = {64, 8, panels, rows / 8, n_blocks};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, rows * row};
+  const cuuint32_t box[5] = {64, 8, panels, box_groups, 1};
+  return encode_map(m, base, 5, dims, strides, box);
 }
 
 int geometry(const prsink_layout* L, Geometry* g) {

@@ -26,12 +26,36 @@ struct Geometry {                            // derived token counts of a layout
 };
 int geometry(const prsink_layout* L, Geometry* g);   // validates, PRSINK_OK or ERR_ARG
 
+// Launch with programmatic stream serialisation: the kernel may start while the one before it
+// finishes, and calls grid_dependency_wait() before it touches global memory.
+template <typename... KArgs, typename... Args>
+inline void launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, int smem,
+                             cudaStream_t st, const Args&... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);     // the error is read by check_launch
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // 3-D bf16 TMA tensor map (dims d0 x d1 x d2, strides in bytes for dims 1 and 2) with a
 // 64 x box1 x box2 box, 128-byte swizzle, zero fill out of bounds.  PRSINK_OK or ERR_LAUNCH.
 int make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
              uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box1, uint32_t box2);
+
+// 5-D bf16 map of rows of D elements in blocks (n_blocks blocks of `rows` rows, contiguous):
+// dimensions (64 elements, 8 rows, D / 64 panels, rows / 8 groups, block), box 64 x 8 x D/64 x
+// box_groups x 1.  One box lands both panels of its rows, as 1 KB swizzle atoms [group][panel].
+int make_map_rows(CUtensorMap* m, const void* base, int D, uint64_t rows, uint64_t n_blocks,
+                  uint32_t box_groups);
 
 // ------------------------------------------------------------------------------------------
 // device side
@@ -134,6 +158,23 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];"
       :: "r"(dst), "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, uint32_t bar, int c0,
+                                            int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+      :: "r"(dst), "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4) : "memory");
+}
+
+// Programmatic dependent launch: wait until the kernels before this one in the stream have
+// completed and their writes are visible / let the next kernel's blocks start early.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // TMA: 3-D tiled store from shared memory (bulk-group completion).  The tile must have been
