@@ -202,8 +202,24 @@ constexpr int kMaxStages = 6;
 constexpr int kMetaRing = 16;              // tiles whose bad-page bits are kept
 constexpr float kRescale = 8.0f;           // log2 units: O is rescaled when a maximum grows > 2^8
 
+// Quotient by a constant of the call: q = (n + hi(n m)) >> s for 0 <= n < 2^31, with 2^s the next
+// power of two >= d and m = floor(2^32 (2^s - d) / d) + 1.
+struct Divisor {
+  uint32_t m, s;
+  void set(uint32_t d) {
+    s = 0;
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>((((1ull << s) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((static_cast<uint32_t>(n) + __umulhi(static_cast<uint32_t>(n), m)) >> s);
+  }
+};
+
 struct AttParams {
   Cache c;
+  Divisor by_tile;                         // tokens of a tile (small pages) or of a page
+  Divisor by_tiles_per_page, by_chunks;
   int group, chunks;                       // query heads per key head, N-column chunks of them
   int tile_tokens, pages_per_tile;         // of a tile when pages are smaller than a tile
   int tiles_per_page;                      // tiles of a page when pages are larger (else 0)
@@ -247,9 +263,8 @@ struct Smem {
 struct Row {
   int len, sink, win0, n_a, first_b, count;
   __device__ __forceinline__ static int tile_of(const AttParams& p, int token) {
-    if (!p.tiles_per_page) return token / p.tile_tokens;
-    const int page = token / p.c.page_size;
-    return page * p.tiles_per_page + (token - page * p.c.page_size) / kTile;
+    const int x = p.by_tile(token);
+    return p.tiles_per_page ? x * p.tiles_per_page + (token - x * p.c.page_size) / kTile : x;
   }
   __device__ __forceinline__ Row(const AttParams& p, int n) {
     len = n;
@@ -285,7 +300,7 @@ struct Tile {
       sub = 0;
       cnt = p.tile_tokens;
     } else {
-      page = t / p.tiles_per_page;
+      page = p.by_tiles_per_page(t);
       sub = (t - page * p.tiles_per_page) * kTile;
       cnt = min(kTile, p.c.page_size - sub);
     }
@@ -329,20 +344,18 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
 }
 
 // A CTA's share of the units, row by row; every role walks it on its own.
+struct Start {
+  int s, hc, i0, len;                      // sequence, head chunk, tile, the sequence's length
+};
+
 struct Walk {
   long long left;                          // units left, this segment's included
   int s, hc, i0, n;                        // sequence, head chunk, first tile, tiles here
   Row row;
   bool first;                              // the CTA's first segment
-  __device__ __forceinline__ Walk(const AttParams& p, int s0, long long off, long long units)
-      : left(units), s(s0), hc(0), i0(0), n(0), row(p, 0), first(true) {
-    if (left > 0) {
-      row = Row(p, seq_len(p.c, s));
-      if (row.count == 0) { left = 0; return; }            // (lengths changed under the call)
-      hc = static_cast<int>(quot(off, row.count));
-      i0 = static_cast<int>(off - static_cast<long long>(hc) * row.count);
-      take();
-    }
+  __device__ __forceinline__ Walk(const AttParams& p, const Start& at, long long units)
+      : left(units), s(at.s), hc(at.hc), i0(at.i0), n(0), row(p, at.len), first(true) {
+    take();
   }
   __device__ __forceinline__ void take() {
     n = static_cast<int>(min(left, static_cast<long long>(row.count - i0)));
@@ -390,6 +403,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
+}
+
 // KFULL / VFULL: a stage has landed.  SDONE: the S product of the tile in K stage i is done (its
 // scores may be read, the stage refilled); ODONE: likewise the O product of V stage i (O holds
 // the tile, P and the stage are free).  SFREE: the scores of a buffer have been read.
@@ -425,18 +443,22 @@ struct Share {
   }
 };
 
-// The sequence that holds unit `begin(cta)` and the unit's offset in it, by a block-wide scan
-// over the lengths (consecutive sequences per thread).  Two barriers; `warp_s` one word per warp.
+// Where unit `begin(cta)` lies, by a block-wide scan over the lengths (consecutive sequences per
+// thread).  Two barriers; `warp_s` one word per warp.
 template <int kThreads>
 __device__ __forceinline__ Share find_share(const AttParams& p, int cta, long long* warp_s,
-                                            int* seq_s, long long* off_s) {
+                                            Start* at_s) {
   const int hcs = p.c.Hkv * p.chunks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (p.c.n_seqs + kThreads - 1) / kThreads;
   const int sa = min(p.c.n_seqs, static_cast<int>(threadIdx.x) * per);
   const int se = min(p.c.n_seqs, sa + per);
   long long mine = 0;
-  for (int s = sa; s < se; ++s) mine += Row(p, seq_len(p.c, s)).count;
+  int len = 0;
+  for (int s = sa; s < se; ++s) {
+    len = seq_len(p.c, s);
+    mine += Row(p, len).count;
+  }
   mine *= hcs;
   long long incl = mine;
 #pragma unroll
@@ -456,15 +478,19 @@ __device__ __forceinline__ Share find_share(const AttParams& p, int cta, long lo
   const long long u0 = sh.begin(cta);
   if (u0 >= before && u0 < before + mine) {
     long long off = u0 - before;
-    for (int s = sa; s < se; ++s) {
-      const long long n = static_cast<long long>(Row(p, seq_len(p.c, s)).count) * hcs;
-      if (off < n) {
-        *seq_s = s;
-        *off_s = off;
-        break;
+    int s = sa;
+    int count = Row(p, len).count;
+    if (per > 1)
+      for (;; ++s) {
+        len = seq_len(p.c, s);
+        count = Row(p, len).count;
+        const long long n = static_cast<long long>(count) * hcs;
+        if (off < n || s + 1 >= se) break;
+        off -= n;
       }
-      off -= n;
-    }
+    count = max(count, 1);
+    const int hc = static_cast<int>(quot(off, count));
+    *at_s = Start{s, hc, static_cast<int>(off - static_cast<long long>(hc) * count), len};
   }
   __syncthreads();
   return sh;
@@ -485,8 +511,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
   __shared__ __align__(16) float m_s[N];           // the heads' running offsets (log2 units)
   __shared__ __align__(16) float alpha_s[N];       // what a new offset rescales by
   __shared__ __align__(16) float red_s[4][N];      // per warp: tile maxima, then sums
-  __shared__ long long scan_s[kAttThreads / 32], off_s;
-  __shared__ int start_s;
+  __shared__ long long scan_s[kAttThreads / 32];
+  __shared__ Start start_s;
   __shared__ int loads_s[3];                       // Q, K and V loads sent (for the drain)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(dsmem);
@@ -509,8 +535,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       mbar_init(bar(B_FINAL + i), 1);
     }
     ab.flag = 0;
-    start_s = 0;
-    off_s = 0;
+    start_s = Start{};
     loads_s[0] = loads_s[1] = loads_s[2] = 0;
     fence_barrier_init();
   }
@@ -535,12 +560,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
   grid_dependency_wait();
   grid_launch_dependents();
   const int cta = blockIdx.x;
-  const Share sh = find_share<kAttThreads>(p, cta, scan_s, &start_s, &off_s);
+  const Share sh = find_share<kAttThreads>(p, cta, scan_s, &start_s);
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   const uint64_t deadline = globaltimer() + p.timeout_ns;
   const long long u1 = sh.begin(cta + 1);
-  Walk w(p, start_s, off_s, u1 - sh.begin(cta));
+  Walk w(p, start_s, u1 - sh.begin(cta));
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------- TMA producer
@@ -572,7 +597,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
     };
     for (; ok && w.left > 0; w.next(p), ++seg) {
       const int* table = p.c.table + static_cast<long long>(w.s) * p.c.max_pages;
-      const int kvh = w.hc / p.chunks, chunk = w.hc - kvh * p.chunks;
+      const int kvh = p.by_chunks(w.hc), chunk = w.hc - kvh * p.chunks;
       if (seg >= 2)
         ok = mbar_wait(bar(B_QFREE + (seg & 1)), ((seg >> 1) - 1) & 1, &ab, deadline, p.c.status);
       if (!__all_sync(~0u, ok)) { ok = false; break; }
@@ -583,36 +608,54 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
                       bar(B_QFULL + (seg & 1)), pp * 64, chunk * N, w.s * p.c.Hkv + kvh);
         loads_s[0] = seg + 1;
       }
-      Tile tile(p, w.row, w.i0);
-      for (int i = 0; ok && i < w.n; ++i, ++j, tile.next(p, w.row)) {
-        // this lane's page
-        const int page_no = tile.page + lane;
-        const int first = tile.start + lane * p.c.page_size;
-        bool need = lane < p.pages_per_tile;
-        need = need && (first < w.row.sink ||
-                        (first + p.c.page_size > w.row.win0 && first < w.row.len));
-        int c2 = -1;
-        bool bad = false;
-        if (need) {
-          int page = table[page_no];
-          bad = page < 0 || page >= p.c.n_pages;
-          if (bad) page = p.c.n_pages;             // past the pool: the box is filled with zeros
-          c2 = bad ? page * p.c.Hkv : page * p.c.Hkv + kvh;
+      // Table entries are read 32 at a time, a batch ahead of their use: lane l holds page
+      // l % pages_per_tile of tile base + l / pages_per_tile.
+      const int ppt = p.pages_per_tile, batch = 32 / ppt;
+      const int my_tile = lane / ppt, my_page = lane - my_tile * ppt;
+      int page = 0, row = 0, base = 0;
+      bool need = false;
+      auto fetch = [&](int from, int& e_page, int& e_row, bool& e_need) {
+        e_need = my_tile < batch && from + my_tile < w.n;
+        if (e_need) {
+          const Tile tile(p, w.row, w.i0 + from + my_tile);
+          const int first = tile.start + my_page * p.c.page_size;
+          e_need = first < w.row.sink ||
+                   (first + p.c.page_size > w.row.win0 && first < w.row.len);
+          e_row = tile.sub;
+          if (e_need) e_page = __ldg(table + tile.page + my_page);
         }
+      };
+      int n_page = 0, n_row = 0;
+      bool n_need = false;
+      fetch(0, n_page, n_row, n_need);
+      for (int i = 0; ok && i < w.n; ++i, ++j) {
+        if (i == 0 || i == base + batch) {
+          base = i;
+          page = n_page;
+          row = n_row;
+          need = n_need;
+          fetch(base + batch, n_page, n_row, n_need);
+        }
+        const int src = (i - base) * ppt + lane;
+        int t_page = __shfl_sync(~0u, page, src & 31);
+        const int t_row = __shfl_sync(~0u, row, src & 31);
+        const bool t_need = __shfl_sync(~0u, static_cast<int>(need), src & 31) && lane < ppt;
+        const bool bad = t_need && (t_page < 0 || t_page >= p.c.n_pages);
+        // (a bad page: a box past the pool, which is filled with zeros)
+        const int c2 = t_need ? (bad ? p.c.n_pages * p.c.Hkv : t_page * p.c.Hkv + kvh) : -1;
         const uint32_t bad_mask = __ballot_sync(~0u, bad);
         if (bad_mask && lane == 0) atomicOr(p.c.status, kStatusPage);
-        const int np = __popc(__ballot_sync(~0u, need));
-        const int row = tile.sub;
+        const int np = __popc(__ballot_sync(~0u, t_need));
         if (j >= SM::kKS)
           ok = mbar_wait(bar(B_SDONE + rk.st), rk.parity ^ 1, &ab, deadline, p.c.status);
         if (!__all_sync(~0u, ok)) { ok = false; break; }
         if (lane == 0) bad_pages[j & (kMetaRing - 1)] = static_cast<uint16_t>(bad_mask);
-        load(B_KFULL + rk.st, sb + SM::kK + rk.st * SM::kTileBytes, &tm_k, c2, row, np);
+        load(B_KFULL + rk.st, sb + SM::kK + rk.st * SM::kTileBytes, &tm_k, c2, t_row, np);
         if (lane == 0) loads_s[1] = j + 1;
         rk.next();
         if (j > 0) load_v(j - 1);
         v_c2 = c2;
-        v_row = row;
+        v_row = t_row;
         v_np = np;
       }
     }
@@ -699,7 +742,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       return mbar_wait(bar(B_ODONE + r.st), r.parity, &ab, deadline, p.c.status);
     };
     for (; ok && w.left > 0; w.next(p)) {
-      const int kvh = w.hc / p.chunks, chunk = w.hc - kvh * p.chunks;
+      const int kvh = p.by_chunks(w.hc), chunk = w.hc - kvh * p.chunks;
       const int nh = min(N, p.group - chunk * N);  // heads of this chunk
       float l[N];                                  // this key's share of the heads' sums
 #pragma unroll
@@ -837,47 +880,53 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (ok) ok = o_done(rv1);
       if (!named_bar_and(1, 128, ok)) { ok = false; break; }
       tc_fence_after();
-      uint32_t o[N];
-#pragma unroll
-      for (int c = 0; c < N; c += CH)
-        ld_cols(tmem + lane_off + SM::kColO + c, *reinterpret_cast<uint32_t(*)[CH]>(&o[c]));
+      // sums: each key's shares through the P buffers (free now), a head per warp pass
+      float* part = reinterpret_cast<float*>(gb + SM::kP);
 #pragma unroll
       for (int g = 0; g < N; g += 4) {
         if (g >= nh) break;
-        float x[4] = {l[g], l[g + 1], l[g + 2], l[g + 3]};
 #pragma unroll
-        for (int k = 16; k; k >>= 1)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] += __shfl_xor_sync(~0u, x[e], k);
-        if (lane == 0)
-          *reinterpret_cast<float4*>(&red_s[warp][g]) = make_float4(x[0], x[1], x[2], x[3]);
+        for (int e = 0; e < 4; ++e) part[(g + e) * kTile + t] = l[g + e];
       }
-      tmem_wait_ld();
-      tc_fence_before();
       named_bar_sync(1, 128);
       const long long head0 = static_cast<long long>(w.s) * p.c.H + kvh * p.group + chunk * N;
       const long long slot = (static_cast<long long>(cta) * 2 + (w.first ? 0 : 1)) * N;
       const bool complete = w.n == w.row.count;
-      if (t < nh) {
-        const float lg = (red_s[0][t] + red_s[1][t]) + (red_s[2][t] + red_s[3][t]);
-        if (!complete)
-          p.part_ml[slot + t] = make_float2(m_s[t], lg);
-        else if (p.lse)
-          p.lse[head0 + t] = lg == 0.f ? -INFINITY : (m_s[t] + log2f(lg)) * 0.69314718055994530942f;
-      }
-      if (t < D) {
+#pragma unroll 1
+      for (int g = warp; g < nh; g += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(part + g * kTile + 4 * lane);
+        float lg = (x.x + x.y) + (x.z + x.w);
 #pragma unroll
-        for (int g = 0; g < N; ++g) {
-          if (g >= nh) break;
-          const float og = __uint_as_float(o[g]);
-          if (complete) {
-            const float lg = (red_s[0][g] + red_s[1][g]) + (red_s[2][g] + red_s[3][g]);
-            p.out[(head0 + g) * D + t] = __float2bfloat16_rn(lg == 0.f ? 0.f : __fdividef(og, lg));
-          } else {
-            p.part_o[(slot + g) * D + t] = og;
+        for (int k = 16; k; k >>= 1) lg += __shfl_xor_sync(~0u, lg, k);
+        if (lane == 0) {
+          alpha_s[g] = lg == 0.f ? 0.f : 1.f / lg;
+          if (!complete)
+            p.part_ml[slot + g] = make_float2(m_s[g], lg);
+          else if (p.lse)
+            p.lse[head0 + g] =
+                lg == 0.f ? -INFINITY : (m_s[g] + log2f(lg)) * 0.69314718055994530942f;
+        }
+      }
+      named_bar_sync(1, 128);
+#pragma unroll 1
+      for (int g = 0; g < nh; g += 4) {
+        uint32_t o[4];
+        tmem_ld4(tmem + lane_off + SM::kColO + g, o);
+        tmem_wait_ld();
+        if (t < D) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (g + e >= nh) break;
+            const float og = __uint_as_float(o[e]);
+            if (complete)
+              p.out[(head0 + g + e) * D + t] =
+                  __float2bfloat16_rn(alpha_s[g + e] == 0.f ? 0.f : og * alpha_s[g + e]);
+            else
+              p.part_o[(slot + g + e) * D + t] = og;
           }
         }
       }
+      tc_fence_before();
     }
   }
 
@@ -908,64 +957,78 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 // Block b joins the row that ends in CTA b's share and began in an earlier one's, if there is
 // one:  M = max m,  L = sum l 2^(m - M),  O = sum O 2^(m - M) / L  over its CTAs, in order.  The
-// row is found while the attention kernel still runs.  One head per pass, an element of d per
-// thread.
-constexpr int kJoinThreads = 128;
+// row is found while the attention kernel still runs.  One head per warp, D / 32 elements a lane.
+constexpr int kJoinThreads = 256;
 
 template <int D, int N>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const __grid_constant__ AttParams p) {
-  __shared__ long long scan_s[kJoinThreads / 32], off_s;
-  __shared__ int seq_s;
-  if (threadIdx.x == 0) {
-    seq_s = 0;
-    off_s = 0;
-  }
+  constexpr int E = D / 32;
+  __shared__ long long scan_s[kJoinThreads / 32];
+  __shared__ Start start_s;
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x;
   // (the lengths were there before the attention kernel began)
-  const Share sh = find_share<kJoinThreads>(p, b, scan_s, &seq_s, &off_s);
+  const Share sh = find_share<kJoinThreads>(p, b, scan_s, &start_s);
+  bool shared = false, aligned = false;
+  int c0 = 0, n = 0, nh = 0;
+  long long head0 = 0;
+  if (b > 0 && b < sh.G) {
+    const Start at = start_s;
+    const Row row(p, at.len);
+    const long long u0 = sh.begin(b), a = u0 - at.i0;        // the row's first unit
+    shared = at.i0 > 0 && a + row.count <= sh.begin(b + 1);
+    if (shared) {
+      c0 = sh.cta_of(a);
+      n = b - c0 + 1;
+      aligned = sh.begin(c0) == a;                           // c0's share starts with the row
+      const int kvh = p.by_chunks(at.hc), chunk = at.hc - kvh * p.chunks;
+      nh = min(N, p.group - chunk * N);
+      head0 = static_cast<long long>(at.s) * p.c.H + kvh * p.group + chunk * N;
+    }
+  }
   grid_dependency_wait();
   grid_launch_dependents();
-  if (b == 0 || b >= sh.G) return;
-  const int s = seq_s;
-  const Row row(p, seq_len(p.c, s));
-  if (row.count == 0) return;
-  const long long u0 = sh.begin(b), u1 = sh.begin(b + 1);
-  const int hc = static_cast<int>(quot(off_s, row.count));
-  const long long a = u0 - (off_s - static_cast<long long>(hc) * row.count);   // the row's units
-  if (a == u0 || a + row.count > u1) return;
-  const int c0 = sh.cta_of(a), n = b - c0 + 1;
-  const bool aligned = sh.begin(c0) == a;          // c0's share starts with the row
-  const int kvh = hc / p.chunks, chunk = hc - kvh * p.chunks;
-  const int nh = min(N, p.group - chunk * N);
-  const long long head0 = static_cast<long long>(s) * p.c.H + kvh * p.group + chunk * N;
-  const int sub = threadIdx.x / D, e = threadIdx.x % D;      // D = 64: two heads per pass
-  for (int g = sub; g < nh; g += kJoinThreads / D) {
+  for (int g = threadIdx.x >> 5; g < nh; g += kJoinThreads / 32) {
     auto part = [&](int i) {
       return (static_cast<long long>(c0 + i) * 2 + (i > 0 || aligned ? 0 : 1)) * N + g;
     };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&p.part_ml[part(i)]).x);
+    float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
-    float L = 0.f, acc = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
     for (int i0 = 0; i0 < n; i0 += 32) {
-      float wt = 0.f;
-      if (i0 + lane < n) {
-        const float2 ml = __ldcg(&p.part_ml[part(i0 + lane)]);
-        wt = ml.x > -INFINITY ? ex2(ml.x - M) : 0.f;
-        L += wt * ml.y;
-      }
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < n) ml = __ldcg(&p.part_ml[part(i0 + lane)]);
+      const float top = fmaxf(M, warp_max(ml.x));
+      // (the first batch: nothing to rescale; a batch of empty parts leaves M at -inf)
+      const float scale = M > -INFINITY ? ex2(M - top) : 0.f;
+      const float wt = ml.x > -INFINITY ? ex2(ml.x - top) : 0.f;
+      M = top;
+      L = L * scale + wt * ml.y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= scale;
       const int k = min(32, n - i0);
-#pragma unroll 8
-      for (int i = 0; i < k; ++i)
-        acc += __shfl_sync(~0u, wt, i) * __ldcg(&p.part_o[part(i0 + i) * D + e]);
+#pragma unroll 4
+      for (int i = 0; i < k; ++i) {
+        const float w = __shfl_sync(~0u, wt, i);
+        const float* src = p.part_o + part(i0 + i) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          acc[0] += w * x.x; acc[1] += w * x.y; acc[2] += w * x.z; acc[3] += w * x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          acc[0] += w * x.x; acc[1] += w * x.y;
+        }
+      }
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
-    p.out[(head0 + g) * D + e] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
-    if (p.lse && e == 0)
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (head0 + g) * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      dst[e / 2] = L == 0.f ? 0u : pack2(acc[e] * inv, acc[e + 1] * inv);
+    if (p.lse && lane == 0)
       p.lse[head0 + g] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
   }
 }
@@ -1220,6 +1283,9 @@ extern "C" int prsink_paged_attention(const prsink_paged* paged, const void* q,
   p.pages_per_tile = ps < kTile ? kTile / ps : 1;
   p.tile_tokens = ps < kTile ? p.pages_per_tile * ps : kTile;
   p.box_rows = ps < kTile ? ps : kTile;
+  p.by_tile.set(ps < kTile ? p.tile_tokens : ps);
+  p.by_tiles_per_page.set(p.tiles_per_page ? p.tiles_per_page : 1);
+  p.by_chunks.set(p.chunks);
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
