@@ -193,11 +193,11 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
 // them in CTA order (no counters to clear, no order that depends on timing).
 //
 // A tile holds whole pages up to 128 tokens, or up to 128 tokens of one page; one TMA box per
-// page.  Warps: 0-3 softmax, 4 TMA producer, 5 issues the S products, 6 the O products (one
-// thread issues an MMA in about 45 cycles whatever its size: a tile's 16 small ones are shared).
+// page.  Warps: 0-3 softmax, 4 and 7 send K and V, 5 issues the S products, 6 the O products (one
+// thread issues an MMA in about 45 cycles whatever its size, one warp a box in about 100).
 constexpr int kTile = 128;                 // key rows of a tile = TMEM lanes
-constexpr int kAttThreads = 224;
-constexpr int kProducerWarp = 4, kScoreWarp = 5, kOutWarp = 6;
+constexpr int kAttThreads = 256;
+constexpr int kKeyWarp = 4, kScoreWarp = 5, kOutWarp = 6, kValueWarp = 7;
 constexpr int kMaxStages = 6;
 constexpr int kMetaRing = 16;              // tiles whose bad-page bits are kept
 constexpr float kRescale = 8.0f;           // log2 units: O is rescaled when a maximum grows > 2^8
@@ -539,7 +539,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
     loads_s[0] = loads_s[1] = loads_s[2] = 0;
     fence_barrier_init();
   }
-  if (warp == kProducerWarp && lane == 0) {
+  if (warp == kKeyWarp && lane == 0) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
@@ -567,47 +567,21 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
   const long long u1 = sh.begin(cta + 1);
   Walk w(p, start_s, u1 - sh.begin(cta));
 
-  if (warp == kProducerWarp) {
-    // ------------------------------------------------------------------- TMA producer
-    // K(j), then V(j - 1): the order in which the products take them.  Lane i loads page i of
-    // the tile; pages without an attended token are left alone (their rows are masked).
-    int j = 0, seg = 0;
-    Ring<SM::kKS> rk;
-    Ring<SM::kVS> rv;
+  if (warp == kKeyWarp || warp == kValueWarp) {
+    // ------------------------------------------------------------------- TMA producers
+    // Lane i loads page i of the tile; pages without an attended token are left alone (their
+    // rows are masked).
+    const bool keys = warp == kKeyWarp;
+    const int stages = keys ? SM::kKS : SM::kVS;
+    const int b_full = keys ? B_KFULL : B_VFULL, b_done = keys ? B_SDONE : B_ODONE;
+    const CUtensorMap* tm = keys ? &tm_k : &tm_v;
+    const uint32_t ring = sb + (keys ? SM::kK : SM::kV);
+    int j = 0, seg = 0, st = 0;
+    uint32_t parity = 1;                           // of the phase that frees the stage
     bool ok = true;
-    int v_c2 = -1, v_row = 0, v_np = 0;            // the previous tile's boxes
-    auto load = [&](int full, uint32_t dst, const CUtensorMap* tm, int c2, int row, int np) {
-      if (lane == 0) mbar_arrive_expect_tx(bar(full), np * p.box_rows * D * 2);
-      __syncwarp();
-      if (c2 < 0) return;
-      if (p.one_box) {
-        tma_load_5d(dst + lane * p.box_rows * D * 2, tm, bar(full), 0, 0, 0, row >> 3, c2);
-      } else {                                     // a large page whose rows end inside a group
-        for (int pp = 0; pp < D / 64; ++pp)
-          tma_load_3d(dst + pp * (kTile * 128), tm, bar(full), pp * 64, row, c2);
-      }
-    };
-    auto load_v = [&](int jv) {
-      if (jv >= SM::kVS)
-        ok = mbar_wait(bar(B_ODONE + rv.st), rv.parity ^ 1, &ab, deadline, p.c.status);
-      if (!__all_sync(~0u, ok)) { ok = false; return; }
-      load(B_VFULL + rv.st, sb + SM::kV + rv.st * SM::kTileBytes, &tm_v, v_c2, v_row, v_np);
-      if (lane == 0) loads_s[2] = jv + 1;
-      rv.next();
-    };
     for (; ok && w.left > 0; w.next(p), ++seg) {
       const int* table = p.c.table + static_cast<long long>(w.s) * p.c.max_pages;
       const int kvh = p.by_chunks(w.hc), chunk = w.hc - kvh * p.chunks;
-      if (seg >= 2)
-        ok = mbar_wait(bar(B_QFREE + (seg & 1)), ((seg >> 1) - 1) & 1, &ab, deadline, p.c.status);
-      if (!__all_sync(~0u, ok)) { ok = false; break; }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(B_QFULL + (seg & 1)), N * D * 2);
-        for (int pp = 0; pp < D / 64; ++pp)
-          tma_load_3d(sb + SM::kQ + (seg & 1) * N * D * 2 + pp * N * 128, &tm_q,
-                      bar(B_QFULL + (seg & 1)), pp * 64, chunk * N, w.s * p.c.Hkv + kvh);
-        loads_s[0] = seg + 1;
-      }
       // Table entries are read 32 at a time, a batch ahead of their use: lane l holds page
       // l % pages_per_tile of tile base + l / pages_per_tile.
       const int ppt = p.pages_per_tile, batch = 32 / ppt;
@@ -628,7 +602,20 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       int n_page = 0, n_row = 0;
       bool n_need = false;
       fetch(0, n_page, n_row, n_need);
-      for (int i = 0; ok && i < w.n; ++i, ++j) {
+      if (keys) {
+        if (seg >= 2)
+          ok = mbar_wait(bar(B_QFREE + (seg & 1)), ((seg >> 1) - 1) & 1, &ab, deadline,
+                         p.c.status);
+        if (!__all_sync(~0u, ok)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(B_QFULL + (seg & 1)), N * D * 2);
+          for (int pp = 0; pp < D / 64; ++pp)
+            tma_load_3d(sb + SM::kQ + (seg & 1) * N * D * 2 + pp * N * 128, &tm_q,
+                        bar(B_QFULL + (seg & 1)), pp * 64, chunk * N, w.s * p.c.Hkv + kvh);
+          loads_s[0] = seg + 1;
+        }
+      }
+      for (int i = 0; i < w.n; ++i, ++j) {
         if (i == 0 || i == base + batch) {
           base = i;
           page = n_page;
@@ -637,29 +624,41 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
           fetch(base + batch, n_page, n_row, n_need);
         }
         const int src = (i - base) * ppt + lane;
-        int t_page = __shfl_sync(~0u, page, src & 31);
+        const int t_page = __shfl_sync(~0u, page, src & 31);
         const int t_row = __shfl_sync(~0u, row, src & 31);
         const bool t_need = __shfl_sync(~0u, static_cast<int>(need), src & 31) && lane < ppt;
         const bool bad = t_need && (t_page < 0 || t_page >= p.c.n_pages);
-        // (a bad page: a box past the pool, which is filled with zeros)
-        const int c2 = t_need ? (bad ? p.c.n_pages * p.c.Hkv : t_page * p.c.Hkv + kvh) : -1;
-        const uint32_t bad_mask = __ballot_sync(~0u, bad);
-        if (bad_mask && lane == 0) atomicOr(p.c.status, kStatusPage);
         const int np = __popc(__ballot_sync(~0u, t_need));
-        if (j >= SM::kKS)
-          ok = mbar_wait(bar(B_SDONE + rk.st), rk.parity ^ 1, &ab, deadline, p.c.status);
+        const uint32_t bad_mask = __ballot_sync(~0u, bad);
+        if (j >= stages) ok = mbar_wait(bar(b_done + st), parity, &ab, deadline, p.c.status);
         if (!__all_sync(~0u, ok)) { ok = false; break; }
-        if (lane == 0) bad_pages[j & (kMetaRing - 1)] = static_cast<uint16_t>(bad_mask);
-        load(B_KFULL + rk.st, sb + SM::kK + rk.st * SM::kTileBytes, &tm_k, c2, t_row, np);
-        if (lane == 0) loads_s[1] = j + 1;
-        rk.next();
-        if (j > 0) load_v(j - 1);
-        v_c2 = c2;
-        v_row = t_row;
-        v_np = np;
+        if (lane == 0) {
+          if (keys) {
+            bad_pages[j & (kMetaRing - 1)] = static_cast<uint16_t>(bad_mask);
+            if (bad_mask) atomicOr(p.c.status, kStatusPage);
+          }
+          mbar_arrive_expect_tx(bar(b_full + st), np * p.box_rows * D * 2);
+          loads_s[keys ? 1 : 2] = j + 1;
+        }
+        __syncwarp();
+        if (t_need) {
+          // (a bad page: a box past the pool, which is filled with zeros)
+          const int c2 = bad ? p.c.n_pages * p.c.Hkv : t_page * p.c.Hkv + kvh;
+          const uint32_t dst = ring + st * SM::kTileBytes;
+          if (p.one_box) {
+            tma_load_5d(dst + lane * p.box_rows * D * 2, tm, bar(b_full + st), 0, 0, 0,
+                        t_row >> 3, c2);
+          } else {                                 // a large page whose rows end inside a group
+            for (int pp = 0; pp < D / 64; ++pp)
+              tma_load_3d(dst + pp * (kTile * 128), tm, bar(b_full + st), pp * 64, t_row, c2);
+          }
+        }
+        if (++st == stages) {
+          st = 0;
+          parity ^= 1;
+        }
       }
     }
-    if (ok && j > 0) load_v(j - 1);
   } else if (warp == kScoreWarp) {
     // ------------------------------------------------------------------- S = K Q^T
     if (lane == 0) {
@@ -938,7 +937,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       umma_commit(bar(B_FINAL + (warp == kOutWarp)));
       drain_wait(bar(B_FINAL + (warp == kOutWarp)), 0);
     }
-    if (warp == kProducerWarp && lane == 0) {
+    if (warp == kKeyWarp && lane == 0) {
       for (int i = max(0, loads_s[0] - 2); i < loads_s[0]; ++i)
         drain_wait(bar(B_QFULL + (i & 1)), (i >> 1) & 1);
       for (int i = max(0, loads_s[1] - SM::kKS); i < loads_s[1]; ++i)
