@@ -178,7 +178,8 @@ def _check(rc: int, fn: str):
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # (the raw handle of torch.cuda.current_stream(), without building a Stream object)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -445,13 +446,33 @@ def prsink_attention_fused_split(layout: Layout, q, k_new, v_new, k_rot, k_cache
                            stream, scratch=scratch)
 
 
-def _one_device(fn: str, **tensors):
-    """Every CUDA tensor on the current device (the one whose stream the call is given to)."""
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.is_cuda and \
-                t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{fn}: {name} is on {t.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+def _dptr(t, name: str, dtype, numel, device: int) -> int:
+    """``_ptr`` for a tensor that has to be on the current device (the one whose stream the call
+    is given to)."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
+    if t.get_device() != device:
+        _wrong_device(t, name, device)
+    return t.data_ptr()
+
+
+def _wrong_device(t, name: str, device: int):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+
+
+def _device() -> int:
+    """The current device's index (0 before CUDA is in use: no tensor is on a device then)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
 
 
 def prsink_attention_backward_scratch_bytes(layout: Layout) -> int:
@@ -469,67 +490,64 @@ def prsink_attention_backward(layout: Layout, q, k_cache, v_cache, out, lse, d_o
     ``dk`` / ``dv`` may be None when ``grad_mask`` selects no slot."""
     _, lblk, _, T = prsink_layout_tokens(layout)
     H, d = layout.n_heads, layout.head_dim
-    bf = torch.bfloat16
-    args = (_ptr(q, "q", bf, lblk * H * d), _ptr(k_cache, "k_cache", bf, H * T * d),
-            _ptr(v_cache, "v_cache", bf, H * T * d), _ptr(out, "out", bf, lblk * H * d),
-            _ptr(lse, "lse", torch.float32, H * lblk), _ptr(d_out, "d_out", bf, lblk * H * d),
-            _ptr(dq, "dq", bf, lblk * H * d), _ptr(dk, "dk", bf, H * T * d),
-            _ptr(dv, "dv", bf, H * T * d))
-    _one_device("prsink_attention_backward", q=q, k_cache=k_cache, v_cache=v_cache, out=out,
-                lse=lse, d_out=d_out, dq=dq, dk=dk, dv=dv, scratch=scratch, dyn_src=dyn_src)
+    bf, dev, nq, nk = torch.bfloat16, _device(), lblk * H * d, H * T * d
     rc = _lib.prsink_attention_backward(
-        ctypes.byref(layout), *args, int(grad_mask) & 0xFFFFFFFF,
-        _ptr(dyn_src, "dyn_src", torch.int64, 1), _ptr(scratch, "scratch", torch.uint8),
-        0 if scratch is None else int(scratch.numel()), _stream(stream))
+        ctypes.byref(layout), _dptr(q, "q", bf, nq, dev), _dptr(k_cache, "k_cache", bf, nk, dev),
+        _dptr(v_cache, "v_cache", bf, nk, dev), _dptr(out, "out", bf, nq, dev),
+        _dptr(lse, "lse", torch.float32, H * lblk, dev), _dptr(d_out, "d_out", bf, nq, dev),
+        _dptr(dq, "dq", bf, nq, dev), _dptr(dk, "dk", bf, nk, dev), _dptr(dv, "dv", bf, nk, dev),
+        int(grad_mask) & 0xFFFFFFFF, _dptr(dyn_src, "dyn_src", torch.int64, 1, dev),
+        _dptr(scratch, "scratch", torch.uint8, None, dev),
+        0 if scratch is None else scratch.numel(), _stream(stream))
     _check(rc, "prsink_attention_backward")
 
 
-def _tokens(t, name: str, heads: int, d: int):
+def _tokens(t, name: str, heads: int, d: int, device: int):
     """Pointer, token stride and token count of ``t`` [n][heads][d]: rows of a wider buffer (a
     fused projection's output) are fine, each row itself contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [n_tokens][{heads}][{d}], got {tuple(t.shape)}")
-    n = t.shape[0]
-    if n and ((heads > 1 and t.stride(1) != d) or t.stride(2) != 1):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be [n_tokens][{heads}][{d}], got {tuple(shape)}")
+    n, stride = shape[0], t.stride()
+    if n and ((heads > 1 and stride[1] != d) or stride[2] != 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.data_ptr(), (t.stride(0) if n > 1 else heads * d), n
+    if t.get_device() != device:
+        _wrong_device(t, name, device)
+    return t.data_ptr(), (stride[0] if n > 1 else heads * d), n
 
 
-def _paged_sizes(paged: Paged, k_pages, v_pages, page_table, seq_lens):
+def _paged_ptrs(paged: Paged, k_pages, v_pages, page_table, seq_lens, device: int):
+    n_seqs = paged.n_seqs
     n = paged.n_pages * paged.n_kv_heads * paged.page_size * paged.head_dim
-    return (_ptr(k_pages, "k_pages", torch.bfloat16, n),
-            _ptr(v_pages, "v_pages", torch.bfloat16, n),
-            _ptr(page_table, "page_table", torch.int32, paged.n_seqs * paged.max_pages),
-            _ptr(seq_lens, "seq_lens", torch.int32, paged.n_seqs))
+    return (_dptr(k_pages, "k_pages", torch.bfloat16, n, device),
+            _dptr(v_pages, "v_pages", torch.bfloat16, n, device),
+            _dptr(page_table, "page_table", torch.int32, n_seqs * paged.max_pages, device),
+            _dptr(seq_lens, "seq_lens", torch.int32, n_seqs, device))
 
 
 def prsink_paged_append(paged: Paged, k_new, v_new, k_pages, v_pages, page_table, seq_lens,
                         cu_new=None, q=None, q_rot=None, stream=None):
     """``k_new`` / ``v_new`` / ``q`` [n_tokens][heads][d], their token stride free;
     ``cu_new`` int32 [n_seqs + 1] (None: one token per sequence)."""
-    kp, ks, n = _tokens(k_new, "k_new", paged.n_kv_heads, paged.head_dim)
-    vp, vs, nv = _tokens(v_new, "v_new", paged.n_kv_heads, paged.head_dim)
+    dev, hkv, h, d = _device(), paged.n_kv_heads, paged.n_heads, paged.head_dim
+    kp, ks, n = _tokens(k_new, "k_new", hkv, d, dev)
+    vp, vs, nv = _tokens(v_new, "v_new", hkv, d, dev)
     if nv != n:
         raise ValueError(f"k_new holds {n} tokens, v_new {nv}")
     qp, qs = 0, 0
     if q is not None:
-        qp, qs, nq = _tokens(q, "q", paged.n_heads, paged.head_dim)
+        qp, qs, nq = _tokens(q, "q", h, d, dev)
         if nq != n:
             raise ValueError(f"k_new holds {n} tokens, q {nq}")
-    pools = _paged_sizes(paged, k_pages, v_pages, page_table, seq_lens)
-    cu = _ptr(cu_new, "cu_new", torch.int32, paged.n_seqs + 1)
-    qr = _ptr(q_rot, "q_rot", torch.bfloat16, n * paged.n_heads * paged.head_dim)
-    _one_device("prsink_paged_append", k_new=k_new, v_new=v_new, k_pages=k_pages,
-                v_pages=v_pages, page_table=page_table, seq_lens=seq_lens, cu_new=cu_new, q=q,
-                q_rot=q_rot)
-    rc = _lib.prsink_paged_append(ctypes.byref(paged), kp, vp, ks, vs, *pools, n, cu, qp, qs, qr,
-                                  _stream(stream))
+    rc = _lib.prsink_paged_append(
+        ctypes.byref(paged), kp, vp, ks, vs,
+        *_paged_ptrs(paged, k_pages, v_pages, page_table, seq_lens, dev), n,
+        _dptr(cu_new, "cu_new", torch.int32, paged.n_seqs + 1, dev), qp, qs,
+        _dptr(q_rot, "q_rot", torch.bfloat16, n * h * d, dev), _stream(stream))
     _check(rc, "prsink_paged_append")
 
 
@@ -544,14 +562,12 @@ def prsink_paged_attention_scratch_bytes(paged: Paged) -> int:
 def prsink_paged_attention(paged: Paged, q, k_pages, v_pages, page_table, seq_lens, out, scratch,
                            lse=None, stream=None):
     """``scratch``: a uint8 CUDA tensor of prsink_paged_attention_scratch_bytes(paged) bytes."""
-    n = paged.n_seqs * paged.n_heads
-    qp = _ptr(q, "q", torch.bfloat16, n * paged.head_dim)
-    pools = _paged_sizes(paged, k_pages, v_pages, page_table, seq_lens)
-    op = _ptr(out, "out", torch.bfloat16, n * paged.head_dim)
-    lp = _ptr(lse, "lse", torch.float32, n)
-    _one_device("prsink_paged_attention", q=q, k_pages=k_pages, v_pages=v_pages,
-                page_table=page_table, seq_lens=seq_lens, out=out, scratch=scratch, lse=lse)
+    dev, n = _device(), paged.n_seqs * paged.n_heads
+    nd = n * paged.head_dim
     rc = _lib.prsink_paged_attention(
-        ctypes.byref(paged), qp, *pools, op, lp, _ptr(scratch, "scratch", torch.uint8),
-        0 if scratch is None else int(scratch.numel()), _stream(stream))
+        ctypes.byref(paged), _dptr(q, "q", torch.bfloat16, nd, dev),
+        *_paged_ptrs(paged, k_pages, v_pages, page_table, seq_lens, dev),
+        _dptr(out, "out", torch.bfloat16, nd, dev), _dptr(lse, "lse", torch.float32, n, dev),
+        _dptr(scratch, "scratch", torch.uint8, None, dev),
+        0 if scratch is None else scratch.numel(), _stream(stream))
     _check(rc, "prsink_paged_attention")

@@ -36,11 +36,13 @@ __device__ __forceinline__ int seq_len(const Cache& c, int s) {
 }
 
 // ------------------------------------------------------------------------------------ append
-// HBM-bound copy of n * (H + 2 Hkv) rows of d bf16, K and q rotated on the way.  A CTA takes
-// kTok tokens: their places and the cos / sin of their positions (f64 angles, shared by every
-// head) go to shared memory once, then each thread owns one 16-byte chunk of a row (four pairs,
-// their cos / sin in registers per token) and walks the rows of the token.
+// HBM-bound copy of n * (H + 2 Hkv) rows of d bf16, K and q rotated on the way.  A CTA takes one
+// token, a share of its rows or four tokens; a thread owns one 16-byte chunk of a row, the same
+// chunk of every row it moves.  The loads of the first kBatch rows, which depend on nothing, are sent
+// before the token's place is looked up and the cos / sin of its position (f64 angles, shared by
+// every head) are computed.
 constexpr int kAppendThreads = 256;
+constexpr int kBatch = 8;
 
 struct AppendParams {
   Cache c;
@@ -69,108 +71,151 @@ __device__ __forceinline__ uint4 rotate_chunk(uint4 v, const float2 (&cs)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Position of token i, or -1 (nothing to do), and its row in the pages, or -1 (no page).  One
+// warp; the sequence is found by a 32-way search.
+__device__ __forceinline__ void place_token(const AppendParams& p, int i, int lane, int& pos,
+                                            long long& row) {
+  pos = -1;
+  row = -1;
+  int s = i, back = 1;                     // the token is the back-th last of sequence s
+  if (p.cu) {
+    // the last s with cu[s] <= i, of cu[0 .. n_seqs]
+    int lo = 0, n = p.c.n_seqs + 1;
+    while (n > 1) {
+      const int step = (n + 31) / 32, at = lo + lane * step;
+      const bool below = lane * step < n && p.cu[at] <= i;
+      const int last = 31 - __clz(__ballot_sync(~0u, below) | 1u);
+      n = min(step, n - last * step);
+      lo += last * step;
+    }
+    s = lo;
+    if (s == p.c.n_seqs) return;           // behind the last sequence
+    const int a = p.cu[s], b = p.cu[s + 1];
+    if (i < a || i >= b) {
+      if (lane == 0) atomicOr(p.c.status, kStatusPage);
+      return;
+    }
+    back = b - i;
+  }
+  const int n = p.c.lens[s];
+  if (n < back || n > p.c.capacity) {
+    if ((n != 0 || p.cu) && lane == 0) atomicOr(p.c.status, kStatusPage);     // (0: an idle row)
+    return;
+  }
+  pos = n - back;
+  const int at = pos / p.c.page_size;
+  const int page = p.c.table[static_cast<long long>(s) * p.c.max_pages + at];
+  if (page >= 0 && page < p.c.n_pages)
+    row = static_cast<long long>(page) * p.c.Hkv * p.c.page_size + (pos - at * p.c.page_size);
+  else if (lane == 0)
+    atomicOr(p.c.status, kStatusPage);
+}
+
 template <int D, int kTok>
 __global__ void __launch_bounds__(kAppendThreads)
 paged_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int C = D / 8;                 // 16-byte chunks of a row
   constexpr int R = kAppendThreads / C;    // rows per pass
-  __shared__ int tok_pos[kTok];            // position, or -1: nothing to do
-  __shared__ long long tok_row[kTok];      // (page * Hkv) * page_size + offset, or -1: no page
+  __shared__ int pos_s[kTok];
+  __shared__ long long row_s[kTok];
   __shared__ __align__(16) float2 tab[kTok][D / 2];
-  const int t0 = blockIdx.x * kTok;
-  if (threadIdx.x < kTok) {
-    const int i = t0 + threadIdx.x;
-    int pos = -1;
-    long long row = -1;
-    if (i < p.n_tokens) {
-      int s = -1, back = 1;                // the token is the back-th last of sequence s
-      if (!p.cu) {
-        s = i;
-      } else if (i < p.cu[p.c.n_seqs]) {
-        int lo = 0, hi = p.c.n_seqs;       // the last s with cu[s] <= i
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (p.cu[mid] <= i) lo = mid; else hi = mid;
-        }
-        if (p.cu[lo] <= i && i < p.cu[lo + 1]) {
-          s = lo;
-          back = p.cu[lo + 1] - i;
-        } else {
-          atomicOr(p.c.status, kStatusPage);
-        }
+  const int i0 = blockIdx.x * kTok, n_tok = min(kTok, p.n_tokens - i0);
+  const int c = threadIdx.x % C, r0 = threadIdx.x / C, warp = threadIdx.x >> 5;
+  const int Hq = p.q ? p.c.H : 0, Hkv = p.c.Hkv;
+  // rows of this CTA: an equal share of every token's rows per blockIdx.y
+  const int rows = Hq + 2 * Hkv;
+  const int per = (rows + gridDim.y - 1) / gridDim.y;
+  const int ra = blockIdx.y * per, mine = min(rows, ra + per) - ra;
+  const int items = mine > 0 ? mine * n_tok : 0;           // (token, row) pairs, token-major
+  // this thread's items, R apart: token and row of the next one to load and of the next to store
+  struct Item {
+    int k, tok, r;
+  };
+  auto wrap = [&](Item& it) {
+    if (kTok > 1)
+      while (it.r >= mine) {
+        it.r -= mine;
+        ++it.tok;
       }
-      if (s >= 0) {
-        const int n = p.c.lens[s];
-        pos = n - back;
-        if (n < 0 || n > p.c.capacity || pos < 0) {
-          if (!(n == 0 && !p.cu)) atomicOr(p.c.status, kStatusPage);
-          pos = -1;
-        } else {
-          const int page = p.c.table[static_cast<long long>(s) * p.c.max_pages +
-                                     pos / p.c.page_size];
-          if (page >= 0 && page < p.c.n_pages)
-            row = static_cast<long long>(page) * p.c.Hkv * p.c.page_size + pos % p.c.page_size;
-          else
-            atomicOr(p.c.status, kStatusPage);
-        }
-      }
+  };
+  auto next = [&](Item& it) {
+    it.k += R;
+    it.r += R;
+    wrap(it);
+  };
+  Item ld{r0, 0, r0}, st;
+  if (mine > 0) wrap(ld);
+  st = ld;
+  auto load = [&](const Item& it) {
+    const long long i = i0 + (kTok > 1 ? it.tok : 0);
+    const int r = ra + it.r;
+    const __nv_bfloat16* src =
+        r < Hq ? p.q + i * p.q_stride + r * D
+               : (r < Hq + Hkv ? p.k + i * p.k_stride + (r - Hq) * D
+                               : p.v + i * p.v_stride + (r - Hq - Hkv) * D);
+    return __ldcs(reinterpret_cast<const uint4*>(src) + c);
+  };
+  grid_dependency_wait();
+  grid_launch_dependents();
+  uint4 x[kBatch];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u)
+    if (ld.k < items) {
+      x[u] = load(ld);
+      next(ld);
     }
-    tok_pos[threadIdx.x] = pos;
-    tok_row[threadIdx.x] = row;
+  if (warp < n_tok) {
+    int pos;
+    long long row;
+    place_token(p, i0 + warp, threadIdx.x & 31, pos, row);
+    if ((threadIdx.x & 31) == 0) {
+      pos_s[warp] = pos;
+      row_s[warp] = row;
+    }
   }
   __syncthreads();
   if (p.rope_mode) {
-    for (int e = threadIdx.x; e < kTok * (D / 2); e += kAppendThreads) {
+    for (int e = threadIdx.x; e < n_tok * (D / 2); e += kAppendThreads) {
       const int t = e / (D / 2), j = e % (D / 2);
-      int x = tok_pos[t];
-      if (x < 0) continue;
+      int at = pos_s[t];
+      if (at < 0) continue;
       if (p.rope_mode == 3) {
-        const int f = x / p.L_f, in = x - f * p.L_f, y = in / p.grid_w;
-        x = j < p.rd[0] ? f : (j < p.rd[0] + p.rd[1] ? y : in - y * p.grid_w);
+        const int f = at / p.L_f, in = at - f * p.L_f, y = in / p.grid_w;
+        at = j < p.rd[0] ? f : (j < p.rd[0] + p.rd[1] ? y : in - y * p.grid_w);
       }
-      double sn, cs;
-      sincospi(static_cast<double>(x) * p.inv_pi_freq[j], &sn, &cs);   // exact reduction
-      tab[t][j] = make_float2(static_cast<float>(cs), static_cast<float>(sn));
+      double sn, co;
+      sincospi(static_cast<double>(at) * p.inv_pi_freq[j], &sn, &co);   // exact reduction
+      tab[t][j] = make_float2(static_cast<float>(co), static_cast<float>(sn));
     }
     __syncthreads();
   }
-  const int c = threadIdx.x % C, r0 = threadIdx.x / C;
-  const int Hq = p.q ? p.c.H : 0, Hkv = p.c.Hkv;
-  const int rows = Hq + 2 * Hkv;
-  // rows of this CTA: an equal share of the token's rows per blockIdx.y
-  const int per = (rows + gridDim.y - 1) / gridDim.y;
-  const int ra = blockIdx.y * per, rb = min(rows, ra + per);
-#pragma unroll 1
-  for (int t = 0; t < kTok; ++t) {
-    if (tok_pos[t] < 0) continue;
-    const long long i = t0 + t, row = tok_row[t];
-    float2 cs[4];
-    if (p.rope_mode) {
-      const float4* tp = reinterpret_cast<const float4*>(&tab[t][4 * c]);
-      const float4 a = tp[0], b = tp[1];
-      cs[0] = make_float2(a.x, a.y); cs[1] = make_float2(a.z, a.w);
-      cs[2] = make_float2(b.x, b.y); cs[3] = make_float2(b.z, b.w);
-    }
-#pragma unroll 4
-    for (int r = ra + r0; r < rb; r += R) {
-      const __nv_bfloat16* src;
-      __nv_bfloat16* dst = nullptr;
-      if (r < Hq) {
-        src = p.q + i * p.q_stride + static_cast<long long>(r) * D;
-        dst = p.q_rot + (i * Hq + r) * D;
-      } else if (r < Hq + Hkv) {
-        src = p.k + i * p.k_stride + static_cast<long long>(r - Hq) * D;
-        if (row >= 0) dst = p.k_pages + (row + static_cast<long long>(r - Hq) * p.c.page_size) * D;
-      } else {
-        src = p.v + i * p.v_stride + static_cast<long long>(r - Hq - Hkv) * D;
-        if (row >= 0)
-          dst = p.v_pages + (row + static_cast<long long>(r - Hq - Hkv) * p.c.page_size) * D;
+  const long long head = static_cast<long long>(p.c.page_size) * D;    // a page's next head
+  while (st.k < items) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (st.k >= items) break;
+      const int r = ra + st.r, tok = kTok > 1 ? st.tok : 0;
+      const long long row = row_s[tok];
+      if (p.rope_mode && r < Hq + Hkv) {
+        const float4* tp = reinterpret_cast<const float4*>(&tab[tok][4 * c]);
+        const float4 a = tp[0], b = tp[1];
+        const float2 cs[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w),
+                              make_float2(b.x, b.y), make_float2(b.z, b.w)};
+        x[u] = rotate_chunk(x[u], cs);
       }
-      if (!dst) continue;
-      uint4 x = reinterpret_cast<const uint4*>(src)[c];
-      if (p.rope_mode && r < Hq + Hkv) x = rotate_chunk(x, cs);
-      reinterpret_cast<uint4*>(dst)[c] = x;
+      __nv_bfloat16* dst =
+          r < Hq ? p.q_rot + (static_cast<long long>(i0 + tok) * Hq + r) * D
+                 : (r < Hq + Hkv ? p.k_pages + row * D + (r - Hq) * head
+                                 : p.v_pages + row * D + (r - Hq - Hkv) * head);
+      if (pos_s[tok] >= 0 && (r < Hq || row >= 0)) reinterpret_cast<uint4*>(dst)[c] = x[u];
+      next(st);
     }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (ld.k < items) {
+        x[u] = load(ld);
+        next(ld);
+      }
   }
 }
 
@@ -1108,9 +1153,27 @@ static int check_ptrs(const char* what, std::initializer_list<const void*> bufs,
   return PRSINK_OK;
 }
 
+// Tokens per CTA and CTAs per token, measured on a B200 (one token per CTA / four):
+//   16384 tokens x 56 rows of 256 B (470 MB)   91.9 us / 81.5 us (5.8 TB/s)
+//   2700 tokens x 120 rows (166 MB)            29.8 us (5.6 TB/s) / 38.1 us
+//   64 tokens x 56 rows                         3.7 us / 6.8 us; one token split over 4: 3.3 us
+// Short tokens share a CTA (and the latency of looking up their place) while the grid still fills
+// the device four times over; where there are few tokens, each is split down to one pass of rows.
 template <int D>
 static void launch_append(const AppendParams& p, cudaStream_t st) {
-  paged_append_kernel<D, 1><<<dim3(p.n_tokens, 1), kAppendThreads, 0, st>>>(p);
+  constexpr int R = kAppendThreads / (D / 8);
+  const int rows = (p.q ? p.c.H : 0) + 2 * p.c.Hkv;
+  int n_sm = 148, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (2 * rows <= 7 * R && p.n_tokens >= 16 * n_sm) {
+    launch_dependent(paged_append_kernel<D, 4>, dim3((p.n_tokens + 3) / 4), kAppendThreads, 0, st,
+                     p);
+    return;
+  }
+  int split = 2 * n_sm / p.n_tokens;
+  split = split < 1 ? 1 : (split > (rows + R - 1) / R ? (rows + R - 1) / R : split);
+  launch_dependent(paged_append_kernel<D, 1>, dim3(p.n_tokens, split), kAppendThreads, 0, st, p);
 }
 
 // Columns of the score tile (query heads of a key head, in chunks of at most 64), CTAs and
