@@ -14,7 +14,8 @@ namespace prsink {
 namespace bwd {
 
 constexpr int kMaxSlots = 3 + PRSINK_MAX_RING;
-constexpr int BM = 128;                    // rows of the statistics are padded to this
+constexpr int BM = 128;                    // rows of a tile (= TMEM lanes); statistics are padded
+constexpr int kMaxTiles = 1024;            // key tiles per call, as in the forward
 
 struct Params {
   int H, L_blk, L_pad, T, L_f, grid_w;
@@ -34,6 +35,8 @@ struct Params {
   const __nv_bfloat16* d_out;
   const float* lse;
   const long long* dyn_src;
+  int* status;
+  unsigned long long timeout_ns;
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
@@ -146,84 +149,474 @@ __global__ void __launch_bounds__(256) prep_queries_kernel(const __grid_constant
   }
 }
 
-template <int E>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* src, float (&x)[E]) {
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = __bfloat162float(src[e]);
-}
-template <int E>
-__device__ __forceinline__ float dot_row(const float (&a)[E], const float (&b)[E]) {
-  float x = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) x += a[e] * b[e];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-  return x;
+// -------------------------------------------------------------------------------- the products
+// One kernel for both sides.  A CTA owns 128 rows (its two operand tiles A1, A2 stay in shared
+// memory, its sums in tensor memory) and streams the other side's tiles Y1, Y2 past them:
+//                rows     A1  A2     Y1  Y2     S = A1 Y1^T   dP = A2 Y2^T   sums
+//   kKeys        keys     k~  v      q~  d_out  S^T           dP^T           dV += P Y2, dK += dS Y1
+//   otherwise    queries  q~  d_out  k~  v      S             dP                         dQ += dS Y1
+// so that P and dS come out as [own rows][streamed rows], which is what the A operand of the sums
+// wants: they go back to tensor memory as bf16 in the place of the scores they came from and
+// never touch shared memory.  Seven products of 128 x 128 x d per pair of tiles instead of the
+// five that one pass would need, but no sum crosses a CTA: a fused pass would have to add 64 KB
+// of float32 dQ to global memory per pair, in an order that changes from run to run.
+//
+// Warps 0-7 turn S into P and dP into dS (row = lane, a half of the streamed rows each), warp 8
+// sends the tiles (Y1 through three stages, since both S and the sum read it; Y2 through two),
+// warp 9 issues the MMAs in an order that leaves each conversion two products of time:
+//   kKeys      dV(j)  S(j+1)  dK(j)  dP(j+1)         otherwise  S(j+1)  dP(j+1)  dQ(j)
+constexpr int kThreads = 320;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kY1 = 3, kY2 = 2;            // stages
+
+enum Bar {
+  B_A = 0, B_Y1FULL = 1, B_Y1FREE = B_Y1FULL + kY1, B_Y2FULL = B_Y1FREE + kY1,
+  B_Y2FREE = B_Y2FULL + kY2, B_SFULL = B_Y2FREE + kY2, B_PFULL, B_DPFULL, B_DSFULL = B_DPFULL + 2,
+  B_SUM, B_FINAL, B_COUNT
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = (D / 64) * 16384;         // 128 rows in 128-byte swizzled panels
+  static constexpr int kA1 = 0, kA2 = kTile;
+  static constexpr int kStage1 = 2 * kTile, kStage2 = kStage1 + kY1 * kTile;
+  // statistics of the streamed queries (kKeys: lse per Y1 stage, delta per Y2 stage), or the list
+  // of live key tiles (otherwise)
+  static constexpr int kStat = kStage2 + kY2 * kTile;
+  static constexpr int kStatBytes = (kY1 + kY2) * BM * 4;
+  static constexpr int kBars = kStat + kStatBytes;
+  static constexpr int kBytes = kBars + B_COUNT * 8 + 32;
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+  static constexpr uint32_t kIdescSum = idesc_bf16_f32(128, D, false, true);
+  static_assert(kMaxTiles * 2 <= kStatBytes, "tile list");
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+struct Tail {                              // what follows the barriers in shared memory
+  uint32_t tmem;
+  AbortState ab;
+  int n_live, y1, y2;                      // live tiles; tiles sent (for the drain)
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// One warp per query row: dQ.
-template <int D>
-__global__ void __launch_bounds__(256) dq_kernel(const __grid_constant__ Params p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, i = blockIdx.x * 8 + (threadIdx.x >> 5), h = blockIdx.y;
-  if (i >= p.L_blk) return;
-  const unsigned vm = live_mask(p);
-  float q[E], g[E], k[E], v[E], acc[E] = {};
-  load_row<E>(p.q_rot + (static_cast<size_t>(h) * p.L_blk + i) * D + lane * E, q);
-  load_row<E>(p.d_out + (static_cast<size_t>(i) * p.H + h) * D + lane * E, g);
-  const float l2 = p.lse2[static_cast<size_t>(h) * p.L_pad + i];
-  const float dl = p.delta[static_cast<size_t>(h) * p.L_pad + i];
+// D (+)= A B over 128 streamed rows: A as bf16 pairs in tensor memory, the first 64 rows at `a`,
+// the others 64 columns further; B MN-major in shared memory (2 KB per 16 rows).
+__device__ __forceinline__ void umma_sum128(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p0, p1;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
+      "add.s32 a, %1, 64;\n\tadd.s64 b, %2, 512;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
+      "add.s32 a, %1, 72;\n\tadd.s64 b, %2, 640;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
+      "add.s32 a, %1, 80;\n\tadd.s64 b, %2, 768;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
+      "add.s32 a, %1, 88;\n\tadd.s64 b, %2, 896;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t dl = globaltimer() + 100000000ull;
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() > dl) break;
+}
+
+// Bits 0 / 1 of a key tile: it holds a row of a live slot / also rows that are not live.
+__device__ __forceinline__ int tile_flags(int n, unsigned vm, const Params& p) {
+  const int lo = n * BM, hi = lo + BM, end = min(hi, p.T);
+  bool live = false, full = hi <= p.T;
   for (int s = 0; s < p.n_slots; ++s) {
-    if (!((vm >> s) & 1u)) continue;
-    for (int r = p.slot_start[s]; r < p.slot_start[s + 1]; ++r) {
-      const size_t at = (static_cast<size_t>(h) * p.T + r) * D + lane * E;
-      load_row<E>(p.k_rot + at, k);
-      load_row<E>(p.v + at, v);
-      const float pr = exp2f(dot_row<E>(q, k) * p.scale_log2 - l2);
-      const float ds = pr * (dot_row<E>(g, v) - dl) * p.scale;
-      for (int e = 0; e < E; ++e) acc[e] += ds * k[e];
+    const bool in = p.slot_start[s] < end && p.slot_start[s + 1] > lo;
+    if ((vm >> s) & 1u) live |= in;
+    else full &= !in;
+  }
+  return (live ? 1 : 0) | (full ? 0 : 2);
+}
+
+// 64 elements of a finished row -> bf16 at `dst`, rotated back by `cs` (null: as they are).
+template <int kPairs>
+__device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16* dst, const float2* cs,
+                                          float scale, bool zero) {
+#pragma unroll 1
+  for (int c = 0; c < 2 * kPairs; c += 32) {
+    uint32_t a[32];
+    tmem_ld32(taddr + c, a);
+    tmem_wait_ld();
+    if (!dst) continue;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x0 = __uint_as_float(a[i + 2 * e]) * scale;
+        float x1 = __uint_as_float(a[i + 2 * e + 1]) * scale;
+        if (cs) {
+          const float2 y = turn(x0, x1, __ldcg(cs + (c + i) / 2 + e), -1.f);
+          x0 = y.x;
+          x1 = y.y;
+        }
+        w[e] = zero ? 0u : pack2(x0, x1);
+      }
+      *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  const float2* cs = p.tab + static_cast<size_t>(p.q_row + i) * (D / 2) + lane * (E / 2);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.dq + (static_cast<size_t>(i) * p.H + h) * D) +
-                  lane * (E / 2);
-  for (int e = 0; e < E / 2; ++e) {
-    const float2 y = turn(acc[2 * e], acc[2 * e + 1], cs[e], -1.f);
-    dst[e] = pack2(y.x, y.y);
-  }
 }
 
-// One warp per key row: dK and dV.
-template <int D>
-__global__ void __launch_bounds__(256) dkv_kernel(const __grid_constant__ Params p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, r = blockIdx.x * 8 + (threadIdx.x >> 5), h = blockIdx.y;
-  if (r >= p.T) return;
-  const int s = slot_of(r, p);
-  if (!((p.grad_mask >> s) & 1u)) return;
-  float q[E], g[E], k[E], v[E], ak[E] = {}, av[E] = {};
-  const size_t at = (static_cast<size_t>(h) * p.T + r) * D + lane * E;
-  if ((live_mask(p) >> s) & 1u) {
-    load_row<E>(p.k_rot + at, k);
-    load_row<E>(p.v + at, v);
-    for (int i = 0; i < p.L_blk; ++i) {
-      load_row<E>(p.q_rot + (static_cast<size_t>(h) * p.L_blk + i) * D + lane * E, q);
-      load_row<E>(p.d_out + (static_cast<size_t>(i) * p.H + h) * D + lane * E, g);
-      const float l2 = p.lse2[static_cast<size_t>(h) * p.L_pad + i];
-      const float dl = p.delta[static_cast<size_t>(h) * p.L_pad + i];
-      const float pr = exp2f(dot_row<E>(q, k) * p.scale_log2 - l2);
-      const float ds = pr * (dot_row<E>(g, v) - dl) * p.scale;
-      for (int e = 0; e < E; ++e) {
-        av[e] += pr * g[e];
-        ak[e] += ds * q[e];
+template <int D, bool kKeys>
+__global__ void __launch_bounds__(kThreads, 1)
+products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
+                const __grid_constant__ Params p) {
+  using SM = Smem<D>;
+  constexpr uint32_t kColS = 0, kColDP = 128;
+  constexpr uint32_t kColDV = 256, kColSum = kKeys ? 256 + D : 384;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y, row0 = blockIdx.x * BM;
+  auto bar = [&](int i) { return sb + SM::kBars + i * 8; };
+  Tail* tail = reinterpret_cast<Tail*>(smem + SM::kBars + B_COUNT * 8);
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + SM::kStat);      // (queries only)
+  const unsigned vm = live_mask(p);
+  if (sb & 1023u) {                                  // (the swizzle needs 1 KB atoms; no static
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);    // memory moves the base)
+    return;
+  }
+
+  if (kKeys) {
+    // key rows that need no gradient, or get zeros
+    if (!(tile_flags(blockIdx.x, p.grad_mask, p) & 1)) return;
+    if (!(tile_flags(blockIdx.x, vm, p) & 1)) {
+      for (int i = threadIdx.x; i < BM * (D / 8); i += kThreads) {
+        const int r = row0 + i / (D / 8);
+        if (r >= p.T || !((p.grad_mask >> slot_of(r, p)) & 1u)) continue;
+        const size_t at = (static_cast<size_t>(h) * p.T + r) * (D / 8) + i % (D / 8);
+        reinterpret_cast<uint4*>(p.dk)[at] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(p.dv)[at] = make_uint4(0, 0, 0, 0);
+      }
+      return;
+    }
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(bar(B_A), 1);
+    for (int i = 0; i < kY1; ++i) {
+      mbar_init(bar(B_Y1FULL + i), 1);
+      mbar_init(bar(B_Y1FREE + i), 1);
+    }
+    for (int i = 0; i < kY2; ++i) {
+      mbar_init(bar(B_Y2FULL + i), 1);
+      mbar_init(bar(B_Y2FREE + i), 1);
+    }
+    mbar_init(bar(B_SFULL), 1);
+    mbar_init(bar(B_PFULL), 256);
+    mbar_init(bar(B_DPFULL), 1);
+    mbar_init(bar(B_DPFULL + 1), 1);
+    mbar_init(bar(B_DSFULL), 256);
+    mbar_init(bar(B_SUM), 1);
+    mbar_init(bar(B_FINAL), 1);
+    tail->ab.flag = 0;
+    tail->y1 = tail->y2 = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&tail->tmem), 512);
+    tmem_relinquish();
+  }
+  if (!kKeys && warp == 0) {
+    // the key tiles that hold a live row, in order; bit 15: some of their rows are not live
+    const int n_tiles = (p.T + BM - 1) / BM;
+    int base = 0;
+    for (int n0 = 0; n0 < n_tiles; n0 += 32) {
+      const int f = n0 + lane < n_tiles ? tile_flags(n0 + lane, vm, p) : 0;
+      const uint32_t bal = __ballot_sync(~0u, f & 1);
+      if (f & 1)
+        list[base + __popc(bal & ((1u << lane) - 1u))] =
+            static_cast<uint16_t>((n0 + lane) | ((f & 2) ? 0x8000 : 0));
+      base += __popc(bal);
+    }
+    if (lane == 0) tail->n_live = base;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tail->tmem;
+  AbortState* ab = &tail->ab;
+  const int n = kKeys ? p.L_pad / BM : tail->n_live;     // streamed tiles
+  const uint64_t deadline = globaltimer() + p.timeout_ns;
+
+  if (warp == kProducerWarp) {
+    if (lane == 0 && n > 0) {
+      // rows r.. of the rotated queries, the keys and values (head-major) or d_out (token-major)
+      auto load = [&](int which, uint32_t dst, int b, int r) {
+        const CUtensorMap* tm = which == 0 ? &tm_q : which == 1 ? &tm_k : which == 2 ? &tm_v : &tm_g;
+        for (int pp = 0; pp < D / 64; ++pp)
+          tma_load_3d(dst + pp * 16384, tm, bar(b), pp * 64, which == 3 ? h : r,
+                      which == 3 ? r : h);
+      };
+      mbar_arrive_expect_tx(bar(B_A), 2 * SM::kTile);
+      load(kKeys ? 1 : 0, sb + SM::kA1, B_A, row0);
+      load(kKeys ? 2 : 3, sb + SM::kA2, B_A, row0);
+      constexpr uint32_t stat = kKeys ? BM * 4 : 0;
+      const float* lse2 = p.lse2 + static_cast<size_t>(h) * p.L_pad;
+      const float* delta = p.delta + static_cast<size_t>(h) * p.L_pad;
+      for (int j = 0; j < n; ++j) {
+        const int r = (kKeys ? j : list[j] & 0x7FFF) * BM;
+        const int s1 = j % kY1, s2 = j % kY2;
+        if (j >= kY1 && !mbar_wait(bar(B_Y1FREE + s1), (j / kY1 - 1) & 1, ab, deadline, p.status))
+          break;
+        mbar_arrive_expect_tx(bar(B_Y1FULL + s1), SM::kTile + stat);
+        load(kKeys ? 0 : 1, sb + SM::kStage1 + s1 * SM::kTile, B_Y1FULL + s1, r);
+        if (kKeys) bulk_load(sb + SM::kStat + s1 * stat, lse2 + r, stat, bar(B_Y1FULL + s1));
+        tail->y1 = j + 1;
+        if (j >= kY2 && !mbar_wait(bar(B_Y2FREE + s2), (j / kY2 - 1) & 1, ab, deadline, p.status))
+          break;
+        mbar_arrive_expect_tx(bar(B_Y2FULL + s2), SM::kTile + stat);
+        load(kKeys ? 3 : 2, sb + SM::kStage2 + s2 * SM::kTile, B_Y2FULL + s2, r);
+        if (kKeys)
+          bulk_load(sb + SM::kStat + (kY1 + s2) * stat, delta + r, stat, bar(B_Y2FULL + s2));
+        tail->y2 = j + 1;
       }
     }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && n > 0) {
+      bool ok = mbar_wait(bar(B_A), 0, ab, deadline, p.status);
+      const uint64_t a1 = sdesc_sw128(sb + SM::kA1, 16, 1024), a2 = sdesc_sw128(sb + SM::kA2, 16, 1024);
+      auto product = [&](uint32_t d, uint64_t a, uint32_t y) {
+        const uint64_t b = sdesc_sw128(y, 16, 1024);
+        if constexpr (D == 128) umma_ss_k128(d, a, b, SM::kIdescS);
+        else umma_ss_k64(d, a, b, SM::kIdescS);
+      };
+      auto y1 = [&](int j) { return sb + SM::kStage1 + (j % kY1) * SM::kTile; };
+      auto y2 = [&](int j) { return sb + SM::kStage2 + (j % kY2) * SM::kTile; };
+      auto col_dp = [&](int j) { return tmem + kColDP + (kKeys ? 0 : (j & 1) * 128); };
+      auto score = [&](int j) -> bool {              // S(j)
+        if (!mbar_wait(bar(B_Y1FULL + j % kY1), (j / kY1) & 1, ab, deadline, p.status)) return false;
+        tc_fence_after();
+        product(tmem + kColS, a1, y1(j));
+        umma_commit(bar(B_SFULL));
+        return true;
+      };
+      auto dprob = [&](int j) -> bool {              // dP(j)
+        if (!mbar_wait(bar(B_Y2FULL + j % kY2), (j / kY2) & 1, ab, deadline, p.status)) return false;
+        tc_fence_after();
+        product(col_dp(j), a2, y2(j));
+        umma_commit(bar(B_DPFULL + (kKeys ? 0 : j & 1)));
+        if (!kKeys) umma_commit(bar(B_Y2FREE + j % kY2));
+        return true;
+      };
+      ok = ok && score(0) && dprob(0);
+      for (int j = 0; ok && j < n; ++j) {
+        if (kKeys || j + 1 < n) {                    // P(j) written (keys) / S(j) read (queries)
+          ok = mbar_wait(bar(B_PFULL), j & 1, ab, deadline, p.status);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (kKeys) {
+          umma_sum128(tmem + kColDV, tmem + kColS, sdesc_sw128(y2(j), 16384, 1024), SM::kIdescSum,
+                      j > 0);
+        }
+        if (j + 1 < n && !score(j + 1)) { ok = false; break; }
+        if (!kKeys && j + 1 < n && !dprob(j + 1)) { ok = false; break; }
+        ok = mbar_wait(bar(B_DSFULL), j & 1, ab, deadline, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        umma_sum128(tmem + kColSum, col_dp(j), sdesc_sw128(y1(j), 16384, 1024), SM::kIdescSum,
+                    j > 0);
+        // (keys: dS(j) has been written, so the statistics of both stages have been read as well)
+        umma_commit(bar(B_Y1FREE + j % kY1));
+        if (kKeys) umma_commit(bar(B_Y2FREE + j % kY2));
+        if (kKeys && j + 1 < n && !dprob(j + 1)) { ok = false; break; }
+      }
+      if (ok) umma_commit(bar(B_SUM));
+    }
+    __syncwarp();
+  } else {
+    const int half = warp >> 2;                      // columns half * 64 ..
+    const int row = row0 + (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + kColS + half * 64;
+    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+    const int slot = kKeys && row < p.T ? slot_of(row, p) : 0;
+    const bool live = !kKeys || (row < p.T && ((vm >> slot) & 1u));
+    float2 nlse = make_float2(0.f, 0.f), ndelta = nlse;    // queries: this row's, negated
+    if (!kKeys) {
+      const size_t at = static_cast<size_t>(h) * p.L_pad + row;
+      nlse.x = nlse.y = -__ldcg(p.lse2 + at);
+      ndelta.x = ndelta.y = -__ldcg(p.delta + at);
+    }
+    bool ok = true;
+    int j = 0;
+    for (; j < n; ++j) {
+      ok = mbar_wait(bar(B_SFULL), j & 1, ab, deadline, p.status);
+      if (kKeys)
+        ok = ok && mbar_wait(bar(B_Y1FULL + j % kY1), (j / kY1) & 1, ab, deadline, p.status);
+      if (!__all_sync(~0u, ok)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t s[64];
+      tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+      tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+      tmem_wait_ld();
+      if (!kKeys) {
+        tc_fence_before();
+        mbar_arrive(bar(B_PFULL));
+      }
+      float2 pr[32];
+      const uint32_t stat1 = sb + SM::kStat + (j % kY1) * (BM * 4) + half * 256;
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        float2 l0 = nlse, l1 = nlse;
+        if (kKeys) {
+          const float4 l = lds4(stat1 + c * 4);
+          l0 = make_float2(-l.x, -l.y);
+          l1 = make_float2(-l.z, -l.w);
+        }
+        const float2 e0 = ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                scale2, l0);
+        const float2 e1 = ffma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                scale2, l1);
+        pr[c / 2] = make_float2(ex2(e0.x), ex2(e0.y));
+        pr[c / 2 + 1] = make_float2(ex2(e1.x), ex2(e1.y));
+      }
+      if (kKeys) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] = live ? pack2(pr[c].x, pr[c].y) : 0u;
+        tmem_st32(t_s, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(B_PFULL));
+      }
+      const int dpb = kKeys ? 0 : j & 1;
+      ok = mbar_wait(bar(B_DPFULL + dpb), kKeys ? j & 1 : (j >> 1) & 1, ab, deadline, p.status);
+      if (kKeys)
+        ok = ok && mbar_wait(bar(B_Y2FULL + j % kY2), (j / kY2) & 1, ab, deadline, p.status);
+      if (!__all_sync(~0u, ok)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t t_dp = tmem + lane_off + kColDP + dpb * 128 + half * 64;
+      tmem_ld32(t_dp, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+      tmem_ld32(t_dp + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+      tmem_wait_ld();
+      // rows of the streamed tile that are not live (queries side): their keys' columns
+      uint32_t mask[2] = {~0u, ~0u};
+      if (!kKeys && (list[j] & 0x8000)) {
+        const int lo = (list[j] & 0x7FFF) * BM + half * 64;
+        for (int s2 = 0; s2 <= p.n_slots; ++s2) {
+          if (s2 < p.n_slots && ((vm >> s2) & 1u)) continue;
+          const int a = (s2 < p.n_slots ? p.slot_start[s2] : p.T) - lo;
+          const int e = s2 < p.n_slots ? p.slot_start[s2 + 1] - lo : 64;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int cl = max(a, w * 32), ch = min(e, w * 32 + 32);
+            if (cl < ch)
+              mask[w] &= ~((ch - cl == 32 ? ~0u : ((1u << (ch - cl)) - 1u)) << (cl - w * 32));
+          }
+        }
+      }
+      const uint32_t stat2 = sb + SM::kStat + (kY1 + j % kY2) * (BM * 4) + half * 256;
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        float2 d0 = ndelta, d1 = ndelta;
+        if (kKeys) {
+          const float4 d = lds4(stat2 + c * 4);
+          d0 = make_float2(-d.x, -d.y);
+          d1 = make_float2(-d.z, -d.w);
+        }
+        const float2 x0 = fmul2(pr[c / 2], fadd2(make_float2(__uint_as_float(s[c]),
+                                                             __uint_as_float(s[c + 1])), d0));
+        const float2 x1 = fmul2(pr[c / 2 + 1], fadd2(make_float2(__uint_as_float(s[c + 2]),
+                                                                 __uint_as_float(s[c + 3])), d1));
+        pk[c / 2] = pack2(x0.x, x0.y);
+        pk[c / 2 + 1] = pack2(x1.x, x1.y);
+      }
+      if (kKeys) {
+        if (!live) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = 0u;
+        }
+      } else if ((mask[0] & mask[1]) != ~0u) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const uint32_t b = mask[c >> 4] >> (2 * (c & 15));
+          pk[c] &= ((b & 1u) ? 0xFFFFu : 0u) | ((b & 2u) ? 0xFFFF0000u : 0u);
+        }
+      }
+      tmem_st32(t_dp, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(B_DSFULL));
+    }
+    // the rows' gradients: each half of the warps writes its half of the elements
+    bool have = false;
+    if (__all_sync(~0u, ok) && n > 0) {
+      have = __all_sync(~0u, mbar_wait(bar(B_SUM), 0, ab, deadline, p.status));
+      tc_fence_after();
+    }
+    constexpr int W = D / 2;                         // elements per half
+    const bool mine = kKeys ? row < p.T && ((p.grad_mask >> slot) & 1u) : row < p.L_blk;
+    const uint32_t t_sum = tmem + lane_off + kColSum + half * W;
+    const float2* cs = p.tab + static_cast<size_t>(kKeys ? (row < p.T ? row : 0)
+                                                         : p.q_row + (row < p.L_blk ? row : 0)) *
+                                   (D / 2) + half * (W / 2);
+    const size_t at = (kKeys ? static_cast<size_t>(h) * p.T + row
+                             : static_cast<size_t>(row) * p.H + h) * D + half * W;
+    const bool zero = !have || !live;
+    store_row<W / 2>(t_sum, mine ? (kKeys ? p.dk : p.dq) + at : nullptr, cs, p.scale, zero);
+    if (kKeys)
+      store_row<W / 2>(tmem + lane_off + kColDV + half * W, mine ? p.dv + at : nullptr, nullptr,
+                       1.f, zero);
   }
-  const float2* cs = p.tab + static_cast<size_t>(r) * (D / 2) + lane * (E / 2);
-  for (int e = 0; e < E / 2; ++e) {
-    const float2 y = turn(ak[2 * e], ak[2 * e + 1], cs[e], -1.f);
-    reinterpret_cast<uint32_t*>(p.dk + at)[e] = pack2(y.x, y.y);
-    reinterpret_cast<uint32_t*>(p.dv + at)[e] = pack2(av[2 * e], av[2 * e + 1]);
+
+  tc_fence_before();
+  __syncthreads();
+  if (ab->flag) {
+    // a wait gave up: copies and MMAs in flight end before their memory is released
+    if (warp == kProducerWarp && lane == 0 && n > 0) {
+      drain_wait(bar(B_A), 0);
+      for (int i = max(0, tail->y1 - kY1); i < tail->y1; ++i)
+        drain_wait(bar(B_Y1FULL + i % kY1), (i / kY1) & 1);
+      for (int i = max(0, tail->y2 - kY2); i < tail->y2; ++i)
+        drain_wait(bar(B_Y2FULL + i % kY2), (i / kY2) & 1);
+    }
+    if (warp == kMmaWarp && lane == 0) {
+      umma_commit(bar(B_FINAL));
+      drain_wait(bar(B_FINAL), 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -280,19 +673,44 @@ static void fill(const prsink_layout* L, const Geometry& g, Params& p) {
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
 }
 
+template <int D, bool kKeys>
+static int launch_products(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                           const CUtensorMap& mg, const Params& p, cudaStream_t st) {
+  const char* what = "prsink_attention_backward";
+  static bool allowed[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !allowed[dev]) {
+    if (cudaFuncSetAttribute(products_kernel<D, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem<D>::kBytes) != cudaSuccess)
+      return check_launch(what);
+    if (dev >= 0 && dev < 64) allowed[dev] = true;
+  }
+  const int rows = kKeys ? p.T : p.L_blk;
+  products_kernel<D, kKeys><<<dim3((rows + BM - 1) / BM, p.H), kThreads, Smem<D>::kBytes, st>>>(
+      mq, mk, mv, mg, p);
+  count_launch();
+  return check_launch(what);
+}
+
 template <int D>
 static int launch(const Params& p, cudaStream_t st) {
   constexpr int R = 256 / (D / 8);
   const char* what = "prsink_attention_backward";
+  CUtensorMap mq, mk, mv, mg;
+  const uint64_t row = 2ull * D, H = p.H;
+  int rc = make_map(&mq, p.q_rot, D, p.L_blk, H, row, row * p.L_blk, BM, 1);
+  if (!rc) rc = make_map(&mk, p.k_rot, D, p.T, H, row, row * p.T, BM, 1);
+  if (!rc) rc = make_map(&mv, p.v, D, p.T, H, row, row * p.T, BM, 1);
+  if (!rc) rc = make_map(&mg, p.d_out, D, H, p.L_blk, row, row * H, 1, BM);
+  if (rc) return rc;
   prep_keys_kernel<D><<<(p.T + R - 1) / R, 256, 0, st>>>(p);
   prep_queries_kernel<D><<<dim3(p.L_pad / R, p.H), 256, 0, st>>>(p);
-  dq_kernel<D><<<dim3((p.L_blk + 7) / 8, p.H), 256, 0, st>>>(p);
-  count_launch(3);
-  if (p.grad_mask) {
-    dkv_kernel<D><<<dim3((p.T + 7) / 8, p.H), 256, 0, st>>>(p);
-    count_launch();
-  }
-  return check_launch(what);
+  count_launch(2);
+  rc = check_launch(what);
+  if (!rc) rc = launch_products<D, false>(mq, mk, mv, mg, p, st);
+  if (!rc && p.grad_mask) rc = launch_products<D, true>(mq, mk, mv, mg, p, st);
+  return rc;
 }
 
 }  // namespace bwd
@@ -337,6 +755,10 @@ extern "C" int prsink_attention_backward(const prsink_layout* layout, const void
                 "dyn_src 8-byte aligned", what);
       return PRSINK_ERR_ALIGN;
     }
+  if ((g.T + BM - 1) / BM > kMaxTiles) {
+    set_error("%s: %lld keys exceed the %d-tile limit", what, g.T, kMaxTiles);
+    return PRSINK_ERR_UNSUPPORTED;
+  }
   if (layout->n_heads > 65535) {
     set_error("%s: %d heads exceed the limit of 65535", what, layout->n_heads);
     return PRSINK_ERR_UNSUPPORTED;
@@ -365,6 +787,9 @@ extern "C" int prsink_attention_backward(const prsink_layout* layout, const void
   p.k_rot = reinterpret_cast<__nv_bfloat16*>(base + pl.k_rot);
   p.q_rot = reinterpret_cast<__nv_bfloat16*>(base + pl.q_rot);
   p.tab = reinterpret_cast<float2*>(base + pl.tab);
+  p.status = status_word_ptr();
+  if (!p.status) return PRSINK_ERR_LAUNCH;
+  p.timeout_ns = 2000000000ull;
   p.lse2 = reinterpret_cast<float*>(base + pl.lse2);
   p.delta = reinterpret_cast<float*>(base + pl.delta);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
