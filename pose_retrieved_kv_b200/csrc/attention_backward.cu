@@ -44,8 +44,8 @@ struct Params {
   __nv_bfloat16* k_rot;                    // [H][T][d], rows of empty slots zero
   __nv_bfloat16* q_rot;                    // [H][L_blk][d]
   float2* tab;                             // [T][d/2] (cos, sin) of every key row's position
-  float* lse2;                             // [H][L_pad] lse in log2 units; +inf: no probability
-  float* delta;                            // [H][L_pad]
+  float* nlse;                             // [H][L_pad] -lse in log2 units; -inf: no probability
+  float* ndelta;                           // [H][L_pad] -delta
 };
 
 __device__ __forceinline__ int slot_of(int row, const Params& p) {
@@ -139,13 +139,13 @@ __global__ void __launch_bounds__(256) prep_queries_kernel(const __grid_constant
 #pragma unroll
   for (int o = C / 2; o; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
   if (c == 0 && i < p.L_pad) {
-    float l = INFINITY;
+    float l = -INFINITY;                             // padding, or a row without keys
     if (i < p.L_blk) {
-      l = p.lse[static_cast<size_t>(h) * p.L_blk + i] * 1.4426950408889634f;
-      if (!(l > -INFINITY)) l = INFINITY;            // a row without keys
+      l = p.lse[static_cast<size_t>(h) * p.L_blk + i] * -1.4426950408889634f;
+      if (l == INFINITY) l = -INFINITY;
     }
-    p.lse2[static_cast<size_t>(h) * p.L_pad + i] = l;
-    p.delta[static_cast<size_t>(h) * p.L_pad + i] = dot;
+    p.nlse[static_cast<size_t>(h) * p.L_pad + i] = l;
+    p.ndelta[static_cast<size_t>(h) * p.L_pad + i] = -dot;
   }
 }
 
@@ -163,16 +163,21 @@ __global__ void __launch_bounds__(256) prep_queries_kernel(const __grid_constant
 //
 // Warps 0-7 turn S into P and dP into dS (row = lane, a half of the streamed rows each), warp 8
 // sends the tiles (Y1 through three stages, since both S and the sum read it; Y2 through two),
-// warp 9 issues the MMAs in an order that leaves each conversion two products of time:
-//   kKeys      dV(j)  S(j+1)  dK(j)  dP(j+1)         otherwise  S(j+1)  dP(j+1)  dQ(j)
+// warp 9 issues the MMAs:
+//   dV(j) (keys)  S(j+1)  |  sum(j)  dP(j+1)  |  ...
+// Every wait or commit of the issuing thread costs the tensor pipe about 100 cycles (it runs only
+// a few MMAs ahead), so there are two of each per pair of tiles: the gate before dV(j) opens when
+// P(j) is written (queries: S(j) read) AND Y1(j+1) has landed, the gate before sum(j) when dS(j)
+// is written and Y2(j+1) has landed (the TMA's bytes and the warps' arrivals count on one
+// barrier), and the commit of dP(j+1), which follows sum(j), also tells the producer that the
+// stages of tile j are free.
 constexpr int kThreads = 320;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr int kY1 = 3, kY2 = 2;            // stages
 
 enum Bar {
-  B_A = 0, B_Y1FULL = 1, B_Y1FREE = B_Y1FULL + kY1, B_Y2FULL = B_Y1FREE + kY1,
-  B_Y2FREE = B_Y2FULL + kY2, B_SFULL = B_Y2FREE + kY2, B_PFULL, B_DPFULL, B_DSFULL = B_DPFULL + 2,
-  B_SUM, B_FINAL, B_COUNT
+  B_A = 0, B_GATE1 = 1, B_GATE2 = B_GATE1 + kY1, B_SFULL = B_GATE2 + kY2, B_DPFULL, B_SUM, B_TAB, B_FINAL,
+  B_COUNT
 };
 
 template <int D>
@@ -195,14 +200,8 @@ struct Smem {
 struct Tail {                              // what follows the barriers in shared memory
   uint32_t tmem;
   AbortState ab;
-  int n_live, y1, y2;                      // live tiles; tiles sent (for the drain)
+  int n_live, y1, y2, tab;                 // live tiles; tiles sent (for the drain)
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // D (+)= A B over 128 streamed rows: A as bf16 pairs in tensor memory, the first 64 rows at `a`,
 // the others 64 columns further; B MN-major in shared memory (2 KB per 16 rows).
@@ -243,6 +242,17 @@ __device__ __forceinline__ float4 lds4(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ uint4 lds4u(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts4(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+               :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t dl = globaltimer() + 100000000ull;
   while (!mbar_try_wait(bar, parity))
@@ -261,31 +271,43 @@ __device__ __forceinline__ int tile_flags(int n, unsigned vm, const Params& p) {
   return (live ? 1 : 0) | (full ? 0 : 2);
 }
 
-// 64 elements of a finished row -> bf16 at `dst`, rotated back by `cs` (null: as they are).
-template <int kPairs>
-__device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16* dst, const float2* cs,
-                                          float scale, bool zero) {
+// W finished sums of this thread's row (tensor memory) -> bf16 in a staged tile (row t, elements
+// from e0 on, 128-byte swizzle), rotated back by the row's cos / sin in `tab` (a tile of 2 D-byte
+// rows in 128-byte panels of two halves; 0: as they are).
+template <int D>
+__device__ __forceinline__ void stage_row(uint32_t taddr, uint32_t dst, int t, int e0,
+                                          uint32_t tab0, uint32_t tab1, float scale) {
+  constexpr int W = D / 2;
 #pragma unroll 1
-  for (int c = 0; c < 2 * kPairs; c += 32) {
-    uint32_t a[32];
-    tmem_ld32(taddr + c, a);
+  for (int c = 0; c < W; c += 16) {
+    uint32_t a[16];
+    tmem_ld16(taddr + c, a);
     tmem_wait_ld();
-    if (!dst) continue;
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
+    for (int i = 0; i < 16; i += 8) {
       uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x0 = __uint_as_float(a[i + 2 * e]) * scale;
-        float x1 = __uint_as_float(a[i + 2 * e + 1]) * scale;
-        if (cs) {
-          const float2 y = turn(x0, x1, __ldcg(cs + (c + i) / 2 + e), -1.f);
-          x0 = y.x;
-          x1 = y.y;
+      for (int e = 0; e < 4; e += 2) {
+        const int pair = (e0 + c + i) / 2 + e;           // even: 16 bytes hold this pair and the next
+        float4 cs = make_float4(1.f, 0.f, 1.f, 0.f);
+        if (tab0) {
+          // panel of 16 pairs; the first half of the panels is in tab0, the other in tab1
+          const int panel = pair >> 4, half = panel / (D / 64), chunk = (pair & 15) >> 1;
+          cs = lds4((half ? tab1 : tab0) + (panel % (D / 64)) * 16384 + t * 128 +
+                    ((chunk ^ (t & 7)) << 4));
         }
-        w[e] = zero ? 0u : pack2(x0, x1);
+        const float x0 = __uint_as_float(a[i + 2 * e]) * scale;
+        const float x1 = __uint_as_float(a[i + 2 * e + 1]) * scale;
+        const float x2 = __uint_as_float(a[i + 2 * e + 2]) * scale;
+        const float x3 = __uint_as_float(a[i + 2 * e + 3]) * scale;
+        const float2 y0 = turn(x0, x1, make_float2(cs.x, cs.y), -1.f);
+        const float2 y1 = turn(x2, x3, make_float2(cs.z, cs.w), -1.f);
+        w[e] = tab0 ? pack2(y0.x, y0.y) : pack2(x0, x1);
+        w[e + 1] = tab0 ? pack2(y1.x, y1.y) : pack2(x2, x3);
       }
-      *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+      const int k = (e0 + c + i) >> 3;                   // 16-byte chunk of the row
+      sts4(dst + (k >> 3) * 16384 + t * 128 + (((k & 7) ^ (t & 7)) << 4),
+           make_uint4(w[0], w[1], w[2], w[3]));
     }
   }
 }
@@ -294,15 +316,16 @@ template <int D, bool kKeys>
 __global__ void __launch_bounds__(kThreads, 1)
 products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
-                const __grid_constant__ Params p) {
+                const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ Params p) {
   using SM = Smem<D>;
   constexpr uint32_t kColS = 0, kColDP = 128;
-  constexpr uint32_t kColDV = 256, kColSum = kKeys ? 256 + D : 384;
+  constexpr uint32_t kColDV = 256, kColSum = kKeys ? 256 + D : 256;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y, row0 = blockIdx.x * BM;
   auto bar = [&](int i) { return sb + SM::kBars + i * 8; };
+  auto tab_stage = [&](int j) { return sb + SM::kStage1 + (j % kY1) * SM::kTile; };
   Tail* tail = reinterpret_cast<Tail*>(smem + SM::kBars + B_COUNT * 8);
   uint16_t* list = reinterpret_cast<uint16_t*>(smem + SM::kStat);      // (queries only)
   const unsigned vm = live_mask(p);
@@ -327,23 +350,15 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   }
   if (threadIdx.x == 0) {
     mbar_init(bar(B_A), 1);
-    for (int i = 0; i < kY1; ++i) {
-      mbar_init(bar(B_Y1FULL + i), 1);
-      mbar_init(bar(B_Y1FREE + i), 1);
-    }
-    for (int i = 0; i < kY2; ++i) {
-      mbar_init(bar(B_Y2FULL + i), 1);
-      mbar_init(bar(B_Y2FREE + i), 1);
-    }
+    for (int i = 0; i < kY1; ++i) mbar_init(bar(B_GATE1 + i), 257);
+    for (int i = 0; i < kY2; ++i) mbar_init(bar(B_GATE2 + i), 257);
     mbar_init(bar(B_SFULL), 1);
-    mbar_init(bar(B_PFULL), 256);
     mbar_init(bar(B_DPFULL), 1);
-    mbar_init(bar(B_DPFULL + 1), 1);
-    mbar_init(bar(B_DSFULL), 256);
     mbar_init(bar(B_SUM), 1);
+    mbar_init(bar(B_TAB), 1);
     mbar_init(bar(B_FINAL), 1);
     tail->ab.flag = 0;
-    tail->y1 = tail->y2 = 0;
+    tail->y1 = tail->y2 = tail->tab = 0;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -385,24 +400,49 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       load(kKeys ? 1 : 0, sb + SM::kA1, B_A, row0);
       load(kKeys ? 2 : 3, sb + SM::kA2, B_A, row0);
       constexpr uint32_t stat = kKeys ? BM * 4 : 0;
-      const float* lse2 = p.lse2 + static_cast<size_t>(h) * p.L_pad;
-      const float* delta = p.delta + static_cast<size_t>(h) * p.L_pad;
-      for (int j = 0; j < n; ++j) {
-        const int r = (kKeys ? j : list[j] & 0x7FFF) * BM;
-        const int s1 = j % kY1, s2 = j % kY2;
-        if (j >= kY1 && !mbar_wait(bar(B_Y1FREE + s1), (j / kY1 - 1) & 1, ab, deadline, p.status))
-          break;
-        mbar_arrive_expect_tx(bar(B_Y1FULL + s1), SM::kTile + stat);
-        load(kKeys ? 0 : 1, sb + SM::kStage1 + s1 * SM::kTile, B_Y1FULL + s1, r);
-        if (kKeys) bulk_load(sb + SM::kStat + s1 * stat, lse2 + r, stat, bar(B_Y1FULL + s1));
-        tail->y1 = j + 1;
-        if (j >= kY2 && !mbar_wait(bar(B_Y2FREE + s2), (j / kY2 - 1) & 1, ab, deadline, p.status))
-          break;
-        mbar_arrive_expect_tx(bar(B_Y2FULL + s2), SM::kTile + stat);
-        load(kKeys ? 3 : 2, sb + SM::kStage2 + s2 * SM::kTile, B_Y2FULL + s2, r);
-        if (kKeys)
-          bulk_load(sb + SM::kStat + (kY1 + s2) * stat, delta + r, stat, bar(B_Y2FULL + s2));
-        tail->y2 = j + 1;
+      const float* nlse = p.nlse + static_cast<size_t>(h) * p.L_pad;
+      const float* ndelta = p.ndelta + static_cast<size_t>(h) * p.L_pad;
+      // (one step past the last tile: the gates behind it open without a copy).  The commits of
+      // dP are waited for one by one: a parity wait is only sound for the next phase.
+      int seen = 0;
+      bool ok = true;
+      for (int j = 0; ok && j <= n; ++j) {
+        const int r = j == n ? 0 : (kKeys ? j : list[j] & 0x7FFF) * BM;
+        const int g1 = bar(B_GATE1 + j % kY1), g2 = bar(B_GATE2 + j % kY2);
+        // Y1(j) takes the stage of tile j - 3, free since the wait before Y2(j - 1)
+        if (j == n) {
+          mbar_arrive(g1);
+        } else {
+          mbar_arrive_expect_tx(g1, SM::kTile + stat);
+          load(kKeys ? 0 : 1, sb + SM::kStage1 + (j % kY1) * SM::kTile, B_GATE1 + j % kY1, r);
+          if (kKeys) bulk_load(sb + SM::kStat + (j % kY1) * stat, nlse + r, stat, g1);
+          tail->y1 = j + 1;
+        }
+        for (; ok && j >= kY2 && seen < j; ++seen)
+          ok = mbar_wait(bar(B_DPFULL), seen & 1, ab, deadline, p.status);
+        if (!ok) break;
+        if (j == n) {
+          mbar_arrive(g2);
+        } else {
+          mbar_arrive_expect_tx(g2, SM::kTile + stat);
+          load(kKeys ? 3 : 2, sb + SM::kStage2 + (j % kY2) * SM::kTile, B_GATE2 + j % kY2, r);
+          if (kKeys) bulk_load(sb + SM::kStat + (kY1 + j % kY2) * stat, ndelta + r, stat, g2);
+          tail->y2 = j + 1;
+        }
+      }
+      if (ok) {
+        // the rows' cos / sin, for the end, into the two Y1 stages that the last tile does not use
+        // (free: the last commit of dP, waited for above, follows the sum of the tile before it)
+        for (; ok && seen < n; ++seen)
+          ok = mbar_wait(bar(B_DPFULL), seen & 1, ab, deadline, p.status);
+        if (ok) {
+          const int r = kKeys ? row0 : p.q_row + row0;
+          mbar_arrive_expect_tx(bar(B_TAB), 2 * SM::kTile);
+          for (int pp = 0; pp < D / 32; ++pp)
+            tma_load_3d(tab_stage(n + pp / (D / 64)) + (pp % (D / 64)) * 16384, &tm_t, bar(B_TAB),
+                        pp * 64, r, 0);
+          tail->tab = 1;
+        }
       }
     }
     __syncwarp();
@@ -417,44 +457,42 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       };
       auto y1 = [&](int j) { return sb + SM::kStage1 + (j % kY1) * SM::kTile; };
       auto y2 = [&](int j) { return sb + SM::kStage2 + (j % kY2) * SM::kTile; };
-      auto col_dp = [&](int j) { return tmem + kColDP + (kKeys ? 0 : (j & 1) * 128); };
-      auto score = [&](int j) -> bool {              // S(j)
-        if (!mbar_wait(bar(B_Y1FULL + j % kY1), (j / kY1) & 1, ab, deadline, p.status)) return false;
-        tc_fence_after();
+      auto gate1 = [&](int j) {
+        return mbar_wait(bar(B_GATE1 + j % kY1), (j / kY1) & 1, ab, deadline, p.status);
+      };
+      auto gate2 = [&](int j) {
+        return mbar_wait(bar(B_GATE2 + j % kY2), (j / kY2) & 1, ab, deadline, p.status);
+      };
+      auto score = [&](int j) {
         product(tmem + kColS, a1, y1(j));
         umma_commit(bar(B_SFULL));
-        return true;
       };
-      auto dprob = [&](int j) -> bool {              // dP(j)
-        if (!mbar_wait(bar(B_Y2FULL + j % kY2), (j / kY2) & 1, ab, deadline, p.status)) return false;
+      auto dprob = [&](int j) {
+        product(tmem + kColDP, a2, y2(j));
+        umma_commit(bar(B_DPFULL));
+      };
+      ok = ok && gate1(0);
+      if (ok) {
         tc_fence_after();
-        product(col_dp(j), a2, y2(j));
-        umma_commit(bar(B_DPFULL + (kKeys ? 0 : j & 1)));
-        if (!kKeys) umma_commit(bar(B_Y2FREE + j % kY2));
-        return true;
-      };
-      ok = ok && score(0) && dprob(0);
+        score(0);
+        ok = gate2(0);
+      }
+      if (ok) {
+        tc_fence_after();
+        dprob(0);
+      }
       for (int j = 0; ok && j < n; ++j) {
-        if (kKeys || j + 1 < n) {                    // P(j) written (keys) / S(j) read (queries)
-          ok = mbar_wait(bar(B_PFULL), j & 1, ab, deadline, p.status);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        if (kKeys) {
+        if (!gate1(j + 1)) { ok = false; break; }
+        tc_fence_after();
+        if (kKeys)
           umma_sum128(tmem + kColDV, tmem + kColS, sdesc_sw128(y2(j), 16384, 1024), SM::kIdescSum,
                       j > 0);
-        }
-        if (j + 1 < n && !score(j + 1)) { ok = false; break; }
-        if (!kKeys && j + 1 < n && !dprob(j + 1)) { ok = false; break; }
-        ok = mbar_wait(bar(B_DSFULL), j & 1, ab, deadline, p.status);
-        if (!ok) break;
+        if (j + 1 < n) score(j + 1);
+        if (!gate2(j + 1)) { ok = false; break; }
         tc_fence_after();
-        umma_sum128(tmem + kColSum, col_dp(j), sdesc_sw128(y1(j), 16384, 1024), SM::kIdescSum,
+        umma_sum128(tmem + kColSum, tmem + kColDP, sdesc_sw128(y1(j), 16384, 1024), SM::kIdescSum,
                     j > 0);
-        // (keys: dS(j) has been written, so the statistics of both stages have been read as well)
-        umma_commit(bar(B_Y1FREE + j % kY1));
-        if (kKeys) umma_commit(bar(B_Y2FREE + j % kY2));
-        if (kKeys && j + 1 < n && !dprob(j + 1)) { ok = false; break; }
+        if (j + 1 < n) dprob(j + 1);
       }
       if (ok) umma_commit(bar(B_SUM));
     }
@@ -465,20 +503,22 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_off + kColS + half * 64;
     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-    const int slot = kKeys && row < p.T ? slot_of(row, p) : 0;
-    const bool live = !kKeys || (row < p.T && ((vm >> slot) & 1u));
     float2 nlse = make_float2(0.f, 0.f), ndelta = nlse;    // queries: this row's, negated
     if (!kKeys) {
       const size_t at = static_cast<size_t>(h) * p.L_pad + row;
-      nlse.x = nlse.y = -__ldcg(p.lse2 + at);
-      ndelta.x = ndelta.y = -__ldcg(p.delta + at);
+      nlse.x = nlse.y = __ldcg(p.nlse + at);
+      ndelta.x = ndelta.y = __ldcg(p.ndelta + at);
     }
     bool ok = true;
-    int j = 0;
-    for (; j < n; ++j) {
+    if (n > 0) {                                     // nothing comes before the first tile
+      mbar_arrive(bar(B_GATE1));
+      mbar_arrive(bar(B_GATE2));
+    }
+    for (int j = 0; j < n; ++j) {
+      const uint32_t next1 = bar(B_GATE1 + (j + 1) % kY1), next2 = bar(B_GATE2 + (j + 1) % kY2);
       ok = mbar_wait(bar(B_SFULL), j & 1, ab, deadline, p.status);
-      if (kKeys)
-        ok = ok && mbar_wait(bar(B_Y1FULL + j % kY1), (j / kY1) & 1, ab, deadline, p.status);
+      if (kKeys)                                     // (open: it let S(j) start; for lse)
+        ok = ok && mbar_wait(bar(B_GATE1 + j % kY1), (j / kY1) & 1, ab, deadline, p.status);
       if (!__all_sync(~0u, ok)) { ok = false; break; }
       tc_fence_after();
       uint32_t s[64];
@@ -487,7 +527,7 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       tmem_wait_ld();
       if (!kKeys) {
         tc_fence_before();
-        mbar_arrive(bar(B_PFULL));
+        mbar_arrive(next1);
       }
       float2 pr[32];
       const uint32_t stat1 = sb + SM::kStat + (j % kY1) * (BM * 4) + half * 256;
@@ -496,8 +536,8 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         float2 l0 = nlse, l1 = nlse;
         if (kKeys) {
           const float4 l = lds4(stat1 + c * 4);
-          l0 = make_float2(-l.x, -l.y);
-          l1 = make_float2(-l.z, -l.w);
+          l0 = make_float2(l.x, l.y);
+          l1 = make_float2(l.z, l.w);
         }
         const float2 e0 = ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
                                 scale2, l0);
@@ -509,19 +549,18 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       if (kKeys) {
         uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = live ? pack2(pr[c].x, pr[c].y) : 0u;
+        for (int c = 0; c < 32; ++c) pk[c] = pack2(pr[c].x, pr[c].y);
         tmem_st32(t_s, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(B_PFULL));
+        mbar_arrive(next1);
       }
-      const int dpb = kKeys ? 0 : j & 1;
-      ok = mbar_wait(bar(B_DPFULL + dpb), kKeys ? j & 1 : (j >> 1) & 1, ab, deadline, p.status);
-      if (kKeys)
-        ok = ok && mbar_wait(bar(B_Y2FULL + j % kY2), (j / kY2) & 1, ab, deadline, p.status);
+      ok = mbar_wait(bar(B_DPFULL), j & 1, ab, deadline, p.status);
+      if (kKeys)                                     // (open likewise; for delta)
+        ok = ok && mbar_wait(bar(B_GATE2 + j % kY2), (j / kY2) & 1, ab, deadline, p.status);
       if (!__all_sync(~0u, ok)) { ok = false; break; }
       tc_fence_after();
-      const uint32_t t_dp = tmem + lane_off + kColDP + dpb * 128 + half * 64;
+      const uint32_t t_dp = tmem + lane_off + kColDP + half * 64;
       tmem_ld32(t_dp, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
       tmem_ld32(t_dp + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
       tmem_wait_ld();
@@ -548,8 +587,8 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         float2 d0 = ndelta, d1 = ndelta;
         if (kKeys) {
           const float4 d = lds4(stat2 + c * 4);
-          d0 = make_float2(-d.x, -d.y);
-          d1 = make_float2(-d.z, -d.w);
+          d0 = make_float2(d.x, d.y);
+          d1 = make_float2(d.z, d.w);
         }
         const float2 x0 = fmul2(pr[c / 2], fadd2(make_float2(__uint_as_float(s[c]),
                                                              __uint_as_float(s[c + 1])), d0));
@@ -558,12 +597,8 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         pk[c / 2] = pack2(x0.x, x0.y);
         pk[c / 2 + 1] = pack2(x1.x, x1.y);
       }
-      if (kKeys) {
-        if (!live) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) pk[c] = 0u;
-        }
-      } else if ((mask[0] & mask[1]) != ~0u) {
+      // (keys side: a row that is not live may hold anything, and spoils only its own sums)
+      if (!kKeys && (mask[0] & mask[1]) != ~0u) {
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           const uint32_t b = mask[c >> 4] >> (2 * (c & 15));
@@ -573,7 +608,7 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       tmem_st32(t_dp, pk);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bar(B_DSFULL));
+      mbar_arrive(next2);
     }
     // the rows' gradients: each half of the warps writes its half of the elements
     bool have = false;
@@ -581,19 +616,39 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       have = __all_sync(~0u, mbar_wait(bar(B_SUM), 0, ab, deadline, p.status));
       tc_fence_after();
     }
-    constexpr int W = D / 2;                         // elements per half
-    const bool mine = kKeys ? row < p.T && ((p.grad_mask >> slot) & 1u) : row < p.L_blk;
-    const uint32_t t_sum = tmem + lane_off + kColSum + half * W;
-    const float2* cs = p.tab + static_cast<size_t>(kKeys ? (row < p.T ? row : 0)
-                                                         : p.q_row + (row < p.L_blk ? row : 0)) *
-                                   (D / 2) + half * (W / 2);
-    const size_t at = (kKeys ? static_cast<size_t>(h) * p.T + row
-                             : static_cast<size_t>(row) * p.H + h) * D + half * W;
-    const bool zero = !have || !live;
-    store_row<W / 2>(t_sum, mine ? (kKeys ? p.dk : p.dq) + at : nullptr, cs, p.scale, zero);
-    if (kKeys)
-      store_row<W / 2>(tmem + lane_off + kColDV + half * W, mine ? p.dv + at : nullptr, nullptr,
-                       1.f, zero);
+    // the sums rotated back (but for dV), rounded and staged in the Y2 stages, which are free now;
+    // then whole rows leave, 2 D bytes at a time, where they are wanted
+    const int t = (warp & 3) * 32 + lane;
+    const uint32_t stage[2] = {sb + SM::kStage2, sb + SM::kStage2 + SM::kTile};
+    if (have) {
+      const bool tab = mbar_wait(bar(B_TAB), 0, ab, deadline, p.status);
+      have = __all_sync(~0u, tab);
+      stage_row<D>(tmem + lane_off + kColSum + half * (D / 2), stage[0], t, half * (D / 2),
+                   tab_stage(n), tab_stage(n + 1), p.scale);
+      if (kKeys)
+        stage_row<D>(tmem + lane_off + kColDV + half * (D / 2), stage[1], t, half * (D / 2), 0, 0,
+                     1.f);
+    }
+    have = named_bar_and(1, 256, have);
+    constexpr int C = D / 8;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < BM * C; i += 256) {
+      const int r = i / C, k = i % C, gr = row0 + r;
+      if (gr >= (kKeys ? p.T : p.L_blk)) continue;
+      const uint32_t off = (k >> 3) * 16384 + r * 128 + (((k & 7) ^ (r & 7)) << 4);
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      if (kKeys) {
+        const int s2 = slot_of(gr, p);
+        if (!((p.grad_mask >> s2) & 1u)) continue;
+        const bool keep = have && ((vm >> s2) & 1u);
+        const size_t at = (static_cast<size_t>(h) * p.T + gr) * C + k;
+        reinterpret_cast<uint4*>(p.dk)[at] = keep ? lds4u(stage[0] + off) : none;
+        reinterpret_cast<uint4*>(p.dv)[at] = keep ? lds4u(stage[1] + off) : none;
+      } else {
+        reinterpret_cast<uint4*>(p.dq)[(static_cast<size_t>(gr) * p.H + h) * C + k] =
+            have ? lds4u(stage[0] + off) : none;
+      }
+    }
   }
 
   tc_fence_before();
@@ -602,10 +657,11 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     // a wait gave up: copies and MMAs in flight end before their memory is released
     if (warp == kProducerWarp && lane == 0 && n > 0) {
       drain_wait(bar(B_A), 0);
+      if (tail->tab) drain_wait(bar(B_TAB), 0);
       for (int i = max(0, tail->y1 - kY1); i < tail->y1; ++i)
-        drain_wait(bar(B_Y1FULL + i % kY1), (i / kY1) & 1);
+        drain_wait(bar(B_GATE1 + i % kY1), (i / kY1) & 1);
       for (int i = max(0, tail->y2 - kY2); i < tail->y2; ++i)
-        drain_wait(bar(B_Y2FULL + i % kY2), (i / kY2) & 1);
+        drain_wait(bar(B_GATE2 + i % kY2), (i / kY2) & 1);
     }
     if (warp == kMmaWarp && lane == 0) {
       umma_commit(bar(B_FINAL));
@@ -622,7 +678,7 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 
 // ---------------------------------------------------------------------------------- host side
 struct Plan {                              // scratch regions, each 256-byte aligned
-  size_t k_rot, q_rot, tab, lse2, delta, total;
+  size_t k_rot, q_rot, tab, nlse, ndelta, total;
 };
 
 static Plan plan(const Geometry& g, int H, int D) {
@@ -632,9 +688,9 @@ static Plan plan(const Geometry& g, int H, int D) {
   p.k_rot = 0;
   p.q_rot = p.k_rot + up(static_cast<size_t>(H) * g.T * D * 2);
   p.tab = p.q_rot + up(static_cast<size_t>(H) * g.L_blk * D * 2);
-  p.lse2 = p.tab + up(static_cast<size_t>(g.T) * (D / 2) * 8);
-  p.delta = p.lse2 + up(H * pad * 4);
-  p.total = p.delta + up(H * pad * 4);
+  p.nlse = p.tab + up(static_cast<size_t>(g.T) * (D / 2) * 8);
+  p.ndelta = p.nlse + up(H * pad * 4);
+  p.total = p.ndelta + up(H * pad * 4);
   return p;
 }
 
@@ -675,7 +731,8 @@ static void fill(const prsink_layout* L, const Geometry& g, Params& p) {
 
 template <int D, bool kKeys>
 static int launch_products(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                           const CUtensorMap& mg, const Params& p, cudaStream_t st) {
+                           const CUtensorMap& mg, const CUtensorMap& mt, const Params& p,
+                           cudaStream_t st) {
   const char* what = "prsink_attention_backward";
   static bool allowed[64] = {false};
   int dev = 0;
@@ -688,7 +745,7 @@ static int launch_products(const CUtensorMap& mq, const CUtensorMap& mk, const C
   }
   const int rows = kKeys ? p.T : p.L_blk;
   products_kernel<D, kKeys><<<dim3((rows + BM - 1) / BM, p.H), kThreads, Smem<D>::kBytes, st>>>(
-      mq, mk, mv, mg, p);
+      mq, mk, mv, mg, mt, p);
   count_launch();
   return check_launch(what);
 }
@@ -697,19 +754,21 @@ template <int D>
 static int launch(const Params& p, cudaStream_t st) {
   constexpr int R = 256 / (D / 8);
   const char* what = "prsink_attention_backward";
-  CUtensorMap mq, mk, mv, mg;
+  CUtensorMap mq, mk, mv, mg, mt;
   const uint64_t row = 2ull * D, H = p.H;
   int rc = make_map(&mq, p.q_rot, D, p.L_blk, H, row, row * p.L_blk, BM, 1);
   if (!rc) rc = make_map(&mk, p.k_rot, D, p.T, H, row, row * p.T, BM, 1);
   if (!rc) rc = make_map(&mv, p.v, D, p.T, H, row, row * p.T, BM, 1);
   if (!rc) rc = make_map(&mg, p.d_out, D, H, p.L_blk, row, row * H, 1, BM);
+  // the table of cos / sin as rows of 4 D bytes
+  if (!rc) rc = make_map(&mt, p.tab, 2 * D, p.T, 1, 2 * row, 2 * row * p.T, BM, 1);
   if (rc) return rc;
   prep_keys_kernel<D><<<(p.T + R - 1) / R, 256, 0, st>>>(p);
   prep_queries_kernel<D><<<dim3(p.L_pad / R, p.H), 256, 0, st>>>(p);
   count_launch(2);
   rc = check_launch(what);
-  if (!rc) rc = launch_products<D, false>(mq, mk, mv, mg, p, st);
-  if (!rc && p.grad_mask) rc = launch_products<D, true>(mq, mk, mv, mg, p, st);
+  if (!rc) rc = launch_products<D, false>(mq, mk, mv, mg, mt, p, st);
+  if (!rc && p.grad_mask) rc = launch_products<D, true>(mq, mk, mv, mg, mt, p, st);
   return rc;
 }
 
@@ -790,8 +849,8 @@ extern "C" int prsink_attention_backward(const prsink_layout* layout, const void
   p.status = status_word_ptr();
   if (!p.status) return PRSINK_ERR_LAUNCH;
   p.timeout_ns = 2000000000ull;
-  p.lse2 = reinterpret_cast<float*>(base + pl.lse2);
-  p.delta = reinterpret_cast<float*>(base + pl.delta);
+  p.nlse = reinterpret_cast<float*>(base + pl.nlse);
+  p.ndelta = reinterpret_cast<float*>(base + pl.ndelta);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return D == 128 ? launch<128>(p, st) : launch<64>(p, st);
 }

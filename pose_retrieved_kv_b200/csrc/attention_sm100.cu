@@ -110,12 +110,6 @@ struct Layout {
   __host__ __device__ static constexpr uint32_t col_o(int qt) { return 256 + qt * D; }
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Softmax exponentials on the FMA pipe for a share of the score columns (column pair i, 0..15,
 // of every 32-column chunk uses the polynomial when bit i of kPolyPairs is set).  Off: measured
 // on a B200 at 480x480, 1/8, 3/16, 1/4 and 1/2 of the exponentials this way were 2-48 % slower,
