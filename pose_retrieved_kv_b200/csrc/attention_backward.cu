@@ -164,20 +164,25 @@ __global__ void __launch_bounds__(256) prep_queries_kernel(const __grid_constant
 // Warps 0-7 turn S into P and dP into dS (row = lane, a half of the streamed rows each), warp 8
 // sends the tiles (Y1 through three stages, since both S and the sum read it; Y2 through two),
 // warp 9 issues the MMAs:
-//   dV(j) (keys)  S(j+1)  |  sum(j)  dP(j+1)  |  ...
+//   kKeys      dV(j) in two halves, S(j+1)  |  dK(j)  dP(j+1)
+//   otherwise  S(j+1)  dP(j+1)              |  dQ(j)              (two buffers of dP)
 // Every wait or commit of the issuing thread costs the tensor pipe about 100 cycles (it runs only
-// a few MMAs ahead), so there are two of each per pair of tiles: the gate before dV(j) opens when
-// P(j) is written (queries: S(j) read) AND Y1(j+1) has landed, the gate before sum(j) when dS(j)
-// is written and Y2(j+1) has landed (the TMA's bytes and the warps' arrivals count on one
-// barrier), and the commit of dP(j+1), which follows sum(j), also tells the producer that the
-// stages of tile j are free.
+// a few MMAs ahead), so there are few of them: a gate opens when the warps have done their part
+// (P(j) written, S(j) read, dS(j) written) AND the tiles that the next products read have landed
+// (the warps' arrivals and the TMA's bytes count on one barrier), and the stages are given back
+// by commits that are there anyway.
 constexpr int kThreads = 320;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr int kY1 = 3, kY2 = 2;            // stages
 
+// GATE1[tile % 3]  Y1 of the tile has landed; the warps have written all of P of the tile before
+//                  it (keys) / read its S, and Y2 has landed as well (queries)
+// PHALF            the warps have written the first half of P (keys)
+// GATE2[tile % 2]  Y2 of the tile has landed (keys); dS of the tile before it is written
+// SFULL, DPFULL[tile % 2]  the product is done (keys: SFULL[0] alone)
 enum Bar {
-  B_A = 0, B_GATE1 = 1, B_GATE2 = B_GATE1 + kY1, B_SFULL = B_GATE2 + kY2, B_DPFULL, B_SUM, B_TAB, B_FINAL,
-  B_COUNT
+  B_A = 0, B_GATE1 = 1, B_GATE2 = B_GATE1 + kY1, B_PHALF = B_GATE2 + kY2, B_SFULL,
+  B_DPFULL = B_SFULL + 2, B_SUM = B_DPFULL + 2, B_TAB, B_FINAL, B_COUNT
 };
 
 template <int D>
@@ -191,7 +196,6 @@ struct Smem {
   static constexpr int kStatBytes = (kY1 + kY2) * BM * 4;
   static constexpr int kBars = kStat + kStatBytes;
   static constexpr int kBytes = kBars + B_COUNT * 8 + 32;
-  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t kIdescSum = idesc_bf16_f32(128, D, false, true);
   static_assert(kMaxTiles * 2 <= kStatBytes, "tile list");
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -203,10 +207,10 @@ struct Tail {                              // what follows the barriers in share
   int n_live, y1, y2, tab;                 // live tiles; tiles sent (for the drain)
 };
 
-// D (+)= A B over 128 streamed rows: A as bf16 pairs in tensor memory, the first 64 rows at `a`,
-// the others 64 columns further; B MN-major in shared memory (2 KB per 16 rows).
-__device__ __forceinline__ void umma_sum128(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t acc) {
+// D (+)= A B over 64 streamed rows: A as bf16 pairs in tensor memory (8 columns per 16 rows), B
+// MN-major in shared memory (2 KB per 16 rows).
+__device__ __forceinline__ void umma_sum64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p0, p1;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
       "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, 0, 0;\n\t"
@@ -216,16 +220,16 @@ __device__ __forceinline__ void umma_sum128(uint32_t d, uint32_t a, uint64_t b, 
       "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
       "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
-      "add.s32 a, %1, 64;\n\tadd.s64 b, %2, 512;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
-      "add.s32 a, %1, 72;\n\tadd.s64 b, %2, 640;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
-      "add.s32 a, %1, 80;\n\tadd.s64 b, %2, 768;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t"
-      "add.s32 a, %1, 88;\n\tadd.s64 b, %2, 896;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p1;\n\t}"
       :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+
+// D = A B^T over the head dimension, both K-major.
+template <int D>
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
+  if constexpr (D == 128) umma_ss_k128(d, a, b, idesc);
+  else umma_ss_k64(d, a, b, idesc);
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -242,6 +246,11 @@ __device__ __forceinline__ float4 lds4(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;"
+               :: "r"(bar), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ uint4 lds4u(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -254,7 +263,7 @@ __device__ __forceinline__ void sts4(uint32_t a, uint4 v) {
 }
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t dl = globaltimer() + 100000000ull;
+  const uint64_t dl = globaltimer() + 5000000ull;
   while (!mbar_try_wait(bar, parity))
     if (globaltimer() > dl) break;
 }
@@ -319,7 +328,7 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ Params p) {
   using SM = Smem<D>;
   constexpr uint32_t kColS = 0, kColDP = 128;
-  constexpr uint32_t kColDV = 256, kColSum = kKeys ? 256 + D : 256;
+  constexpr uint32_t kColDV = 256, kColSum = kKeys ? 256 + D : 384;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -351,9 +360,12 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   if (threadIdx.x == 0) {
     mbar_init(bar(B_A), 1);
     for (int i = 0; i < kY1; ++i) mbar_init(bar(B_GATE1 + i), 257);
-    for (int i = 0; i < kY2; ++i) mbar_init(bar(B_GATE2 + i), 257);
-    mbar_init(bar(B_SFULL), 1);
-    mbar_init(bar(B_DPFULL), 1);
+    for (int i = 0; i < kY2; ++i) {
+      mbar_init(bar(B_GATE2 + i), kKeys ? 257 : 256);
+      mbar_init(bar(B_SFULL + i), 1);
+      mbar_init(bar(B_DPFULL + i), 1);
+    }
+    mbar_init(bar(B_PHALF), 256);
     mbar_init(bar(B_SUM), 1);
     mbar_init(bar(B_TAB), 1);
     mbar_init(bar(B_FINAL), 1);
@@ -390,51 +402,73 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   if (warp == kProducerWarp) {
     if (lane == 0 && n > 0) {
       // rows r.. of the rotated queries, the keys and values (head-major) or d_out (token-major)
-      auto load = [&](int which, uint32_t dst, int b, int r) {
+      auto load = [&](int which, uint32_t dst, uint32_t b, int r) {
         const CUtensorMap* tm = which == 0 ? &tm_q : which == 1 ? &tm_k : which == 2 ? &tm_v : &tm_g;
         for (int pp = 0; pp < D / 64; ++pp)
-          tma_load_3d(dst + pp * 16384, tm, bar(b), pp * 64, which == 3 ? h : r,
+          tma_load_3d(dst + pp * 16384, tm, b, pp * 64, which == 3 ? h : r,
                       which == 3 ? r : h);
       };
       mbar_arrive_expect_tx(bar(B_A), 2 * SM::kTile);
-      load(kKeys ? 1 : 0, sb + SM::kA1, B_A, row0);
-      load(kKeys ? 2 : 3, sb + SM::kA2, B_A, row0);
+      load(kKeys ? 1 : 0, sb + SM::kA1, bar(B_A), row0);
+      load(kKeys ? 2 : 3, sb + SM::kA2, bar(B_A), row0);
       constexpr uint32_t stat = kKeys ? BM * 4 : 0;
       const float* nlse = p.nlse + static_cast<size_t>(h) * p.L_pad;
       const float* ndelta = p.ndelta + static_cast<size_t>(h) * p.L_pad;
-      // (one step past the last tile: the gates behind it open without a copy).  The commits of
-      // dP are waited for one by one: a parity wait is only sound for the next phase.
-      int seen = 0;
+      // Stages: Y1(j) takes the one of tile j - 3, Y2(j) that of tile j - 2.
+      //   keys     dP(j - 1) is issued after dK(j - 2) and dV(j - 2), and frees both; Y1 a step
+      //            ahead.  One step past the last tile opens the gates behind it without a copy.
+      //   queries  dP(j - 2) frees Y2's, S(j - 1), issued after dQ(j - 3), frees Y1's.
+      // (A parity wait is only sound for a barrier's next phase: with one barrier for the even and
+      // one for the odd tiles, the phase after the one waited for needs a tile not yet sent.)
       bool ok = true;
-      for (int j = 0; ok && j <= n; ++j) {
+      auto dp_done = [&](int j) {
+        return mbar_wait(bar(B_DPFULL + (j & 1)), (j >> 1) & 1, ab, deadline, p.status);
+      };
+      for (int j = 0; j <= n; ++j) {
         const int r = j == n ? 0 : (kKeys ? j : list[j] & 0x7FFF) * BM;
-        const int g1 = bar(B_GATE1 + j % kY1), g2 = bar(B_GATE2 + j % kY2);
-        // Y1(j) takes the stage of tile j - 3, free since the wait before Y2(j - 1)
-        if (j == n) {
-          mbar_arrive(g1);
-        } else {
-          mbar_arrive_expect_tx(g1, SM::kTile + stat);
-          load(kKeys ? 0 : 1, sb + SM::kStage1 + (j % kY1) * SM::kTile, B_GATE1 + j % kY1, r);
-          if (kKeys) bulk_load(sb + SM::kStat + (j % kY1) * stat, nlse + r, stat, g1);
-          tail->y1 = j + 1;
-        }
-        for (; ok && j >= kY2 && seen < j; ++seen)
-          ok = mbar_wait(bar(B_DPFULL), seen & 1, ab, deadline, p.status);
-        if (!ok) break;
-        if (j == n) {
-          mbar_arrive(g2);
-        } else {
-          mbar_arrive_expect_tx(g2, SM::kTile + stat);
-          load(kKeys ? 3 : 2, sb + SM::kStage2 + (j % kY2) * SM::kTile, B_GATE2 + j % kY2, r);
-          if (kKeys) bulk_load(sb + SM::kStat + (kY1 + j % kY2) * stat, ndelta + r, stat, g2);
+        const uint32_t g1 = bar(B_GATE1 + j % kY1), g2 = bar(B_GATE2 + j % kY2);
+        const uint32_t to1 = sb + SM::kStage1 + (j % kY1) * SM::kTile;
+        const uint32_t to2 = sb + SM::kStage2 + (j % kY2) * SM::kTile;
+        if (kKeys) {
+          if (j == n) {
+            mbar_arrive(g1);
+          } else {
+            mbar_arrive_expect_tx(g1, SM::kTile + stat);
+            load(0, to1, g1, r);
+            bulk_load(sb + SM::kStat + (j % kY1) * stat, nlse + r, stat, g1);
+            tail->y1 = j + 1;
+          }
+          if (j >= kY2) ok = dp_done(j - 1);
+          if (!ok) break;
+          if (j == n) {
+            mbar_arrive(g2);
+          } else {
+            mbar_arrive_expect_tx(g2, SM::kTile + stat);
+            load(3, to2, g2, r);
+            bulk_load(sb + SM::kStat + (kY1 + j % kY2) * stat, ndelta + r, stat, g2);
+            tail->y2 = j + 1;
+          }
+        } else if (j < n) {
+          if (j >= kY2) ok = dp_done(j - 2);
+          if (!ok) break;
+          mbar_expect_tx(g1, SM::kTile);
+          load(2, to2, g1, r);
           tail->y2 = j + 1;
+          if (j >= kY1)
+            ok = mbar_wait(bar(B_SFULL + ((j - 1) & 1)), ((j - 1) >> 1) & 1, ab, deadline,
+                           p.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(g1, SM::kTile);
+          load(1, to1, g1, r);
+          tail->y1 = j + 1;
         }
       }
       if (ok) {
-        // the rows' cos / sin, for the end, into the two Y1 stages that the last tile does not use
-        // (free: the last commit of dP, waited for above, follows the sum of the tile before it)
-        for (; ok && seen < n; ++seen)
-          ok = mbar_wait(bar(B_DPFULL), seen & 1, ab, deadline, p.status);
+        // the rows' cos / sin, for the end, into the two Y1 stages that the last tile does not
+        // use (the sum of the tile before it, which read the younger of them, is done: keys when
+        // dP(n - 1) is, queries at the end)
+        if (kKeys) ok = n >= kY2 || dp_done(0);
+        else ok = mbar_wait(bar(B_SUM), 0, ab, deadline, p.status);
         if (ok) {
           const int r = kKeys ? row0 : p.q_row + row0;
           mbar_arrive_expect_tx(bar(B_TAB), 2 * SM::kTile);
@@ -449,61 +483,88 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   } else if (warp == kMmaWarp) {
     if (lane == 0 && n > 0) {
       bool ok = mbar_wait(bar(B_A), 0, ab, deadline, p.status);
+      constexpr uint32_t step = SM::kTile >> 4;        // of a stage, in descriptor units
       const uint64_t a1 = sdesc_sw128(sb + SM::kA1, 16, 1024), a2 = sdesc_sw128(sb + SM::kA2, 16, 1024);
-      auto product = [&](uint32_t d, uint64_t a, uint32_t y) {
-        const uint64_t b = sdesc_sw128(y, 16, 1024);
-        if constexpr (D == 128) umma_ss_k128(d, a, b, SM::kIdescS);
-        else umma_ss_k64(d, a, b, SM::kIdescS);
-      };
-      auto y1 = [&](int j) { return sb + SM::kStage1 + (j % kY1) * SM::kTile; };
-      auto y2 = [&](int j) { return sb + SM::kStage2 + (j % kY2) * SM::kTile; };
-      auto gate1 = [&](int j) {
-        return mbar_wait(bar(B_GATE1 + j % kY1), (j / kY1) & 1, ab, deadline, p.status);
-      };
-      auto gate2 = [&](int j) {
-        return mbar_wait(bar(B_GATE2 + j % kY2), (j / kY2) & 1, ab, deadline, p.status);
+      const uint64_t k1 = sdesc_sw128(sb + SM::kStage1, 16, 1024);       // K-major: S, dP
+      const uint64_t k2 = sdesc_sw128(sb + SM::kStage2, 16, 1024);
+      const uint64_t m1 = sdesc_sw128(sb + SM::kStage1, 16384, 1024);    // MN-major: the sums
+      const uint64_t m2 = sdesc_sw128(sb + SM::kStage2, 16384, 1024);
+      // Y1 stage and its gate's parity of tile j + 1, Y1 stage of tile j
+      int s1 = 0, c1 = 0;
+      uint32_t par = 0;
+      auto gate1 = [&]() { return mbar_wait(bar(B_GATE1 + s1), par, ab, deadline, p.status); };
+      auto next = [&]() {
+        c1 = s1;
+        if (++s1 == kY1) {
+          s1 = 0;
+          par ^= 1;
+        }
       };
       auto score = [&](int j) {
-        product(tmem + kColS, a1, y1(j));
-        umma_commit(bar(B_SFULL));
+        product<D>(tmem + kColS, a1, k1 + s1 * step);
+        umma_commit(bar(B_SFULL + (kKeys ? 0 : j & 1)));
       };
       auto dprob = [&](int j) {
-        product(tmem + kColDP, a2, y2(j));
-        umma_commit(bar(B_DPFULL));
+        product<D>(tmem + kColDP + (kKeys ? 0 : (j & 1) * 128), a2, k2 + (j & 1) * step);
+        umma_commit(bar(B_DPFULL + (j & 1)));
       };
-      ok = ok && gate1(0);
+      ok = ok && gate1();
       if (ok) {
         tc_fence_after();
         score(0);
-        ok = gate2(0);
-      }
-      if (ok) {
-        tc_fence_after();
-        dprob(0);
+        next();
+        if (kKeys) {
+          ok = mbar_wait(bar(B_GATE2), 0, ab, deadline, p.status);
+          tc_fence_after();
+        }
+        if (ok) dprob(0);
       }
       for (int j = 0; ok && j < n; ++j) {
-        if (!gate1(j + 1)) { ok = false; break; }
+        const int cur = c1;                            // Y1 stage of tile j
+        if (kKeys) {
+          const uint64_t y2 = m2 + (j & 1) * step;
+          ok = mbar_wait(bar(B_PHALF), j & 1, ab, deadline, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          umma_sum64(tmem + kColDV, tmem + kColS, y2, SM::kIdescSum, j > 0);
+          ok = gate1();
+          if (!ok) break;
+          tc_fence_after();
+          umma_sum64(tmem + kColDV, tmem + kColS + 64, y2 + 512, SM::kIdescSum, 1);
+          if (j + 1 < n) score(j + 1);
+          next();
+          ok = mbar_wait(bar(B_GATE2 + ((j + 1) & 1)), ((j + 1) >> 1) & 1, ab, deadline, p.status);
+        } else {
+          if (j + 1 < n) {
+            ok = gate1();
+            if (!ok) break;
+            tc_fence_after();
+            score(j + 1);
+            next();
+            dprob(j + 1);
+          }
+          ok = mbar_wait(bar(B_GATE2 + (j & 1)), (j >> 1) & 1, ab, deadline, p.status);
+        }
+        if (!ok) break;
         tc_fence_after();
-        if (kKeys)
-          umma_sum128(tmem + kColDV, tmem + kColS, sdesc_sw128(y2(j), 16384, 1024), SM::kIdescSum,
-                      j > 0);
-        if (j + 1 < n) score(j + 1);
-        if (!gate2(j + 1)) { ok = false; break; }
-        tc_fence_after();
-        umma_sum128(tmem + kColSum, tmem + kColDP, sdesc_sw128(y1(j), 16384, 1024), SM::kIdescSum,
-                    j > 0);
-        if (j + 1 < n) dprob(j + 1);
+        const uint32_t ds = tmem + kColDP + (kKeys ? 0 : (j & 1) * 128);
+        umma_sum64(tmem + kColSum, ds, m1 + cur * step, SM::kIdescSum, j > 0);
+        umma_sum64(tmem + kColSum, ds + 64, m1 + cur * step + 512, SM::kIdescSum, 1);
+        if (kKeys && j + 1 < n) dprob(j + 1);
       }
       if (ok) umma_commit(bar(B_SUM));
     }
     __syncwarp();
   } else {
-    const int half = warp >> 2;                      // columns half * 64 ..
+    // Columns of a thread: 32 of the streamed rows 0-63 and 32 of 64-127 (part 0 / 1 of the row).
+    // P and dS of a part go, as bf16 pairs, into the first 32 columns of its 64; the two warps
+    // that share the lanes meet before that, since each writes where the other has read.
+    const int half = warp >> 2;
     const int row = row0 + (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + kColS + half * 64;
+    const uint32_t t_s = tmem + lane_off + kColS;
     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-    float2 nlse = make_float2(0.f, 0.f), ndelta = nlse;    // queries: this row's, negated
+    float2 nlse = make_float2(0.f, 0.f), ndelta = nlse;    // queries: this row's
     if (!kKeys) {
       const size_t at = static_cast<size_t>(h) * p.L_pad + row;
       nlse.x = nlse.y = __ldcg(p.nlse + at);
@@ -512,81 +573,97 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     bool ok = true;
     if (n > 0) {                                     // nothing comes before the first tile
       mbar_arrive(bar(B_GATE1));
-      mbar_arrive(bar(B_GATE2));
+      if (kKeys) mbar_arrive(bar(B_GATE2));
     }
+    int s1 = 0;                                      // j % 3
+    uint32_t par1 = 0;
     for (int j = 0; j < n; ++j) {
-      const uint32_t next1 = bar(B_GATE1 + (j + 1) % kY1), next2 = bar(B_GATE2 + (j + 1) % kY2);
-      ok = mbar_wait(bar(B_SFULL), j & 1, ab, deadline, p.status);
+      const uint32_t gate1 = bar(B_GATE1 + s1), stat1 = sb + SM::kStat + s1 * (BM * 4) + half * 128;
+      const uint32_t gate1_par = par1;
+      if (++s1 == kY1) {
+        s1 = 0;
+        par1 ^= 1;
+      }
+      const uint32_t next1 = bar(B_GATE1 + s1);
+      const uint32_t done2 = bar(B_GATE2 + ((kKeys ? j + 1 : j) & 1));
+      ok = mbar_wait(bar(B_SFULL + (kKeys ? 0 : j & 1)), (kKeys ? j : j >> 1) & 1, ab, deadline,
+                     p.status);
       if (kKeys)                                     // (open: it let S(j) start; for lse)
-        ok = ok && mbar_wait(bar(B_GATE1 + j % kY1), (j / kY1) & 1, ab, deadline, p.status);
-      if (!__all_sync(~0u, ok)) { ok = false; break; }
+        ok = ok && mbar_wait(gate1, gate1_par, ab, deadline, p.status);
+      __syncwarp();
       tc_fence_after();
       uint32_t s[64];
-      tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-      tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+      tmem_ld32(t_s + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+      tmem_ld32(t_s + 64 + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
       tmem_wait_ld();
       if (!kKeys) {
         tc_fence_before();
         mbar_arrive(next1);
       }
+      // (a wait that gave up in one of the two warps ends the loop for both)
+      if (!named_bar_and(2 + (warp & 3), 64, ok)) { ok = false; break; }
       float2 pr[32];
-      const uint32_t stat1 = sb + SM::kStat + (j % kY1) * (BM * 4) + half * 256;
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        float2 l0 = nlse, l1 = nlse;
-        if (kKeys) {
-          const float4 l = lds4(stat1 + c * 4);
-          l0 = make_float2(l.x, l.y);
-          l1 = make_float2(l.z, l.w);
+      for (int part = 0; part < 2; ++part) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const int c = part * 32 + i;
+          float2 l0 = nlse, l1 = nlse;
+          if (kKeys) {
+            const float4 l = lds4(stat1 + part * 256 + i * 4);
+            l0 = make_float2(l.x, l.y);
+            l1 = make_float2(l.z, l.w);
+          }
+          const float2 e0 = ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                  scale2, l0);
+          const float2 e1 = ffma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                  scale2, l1);
+          pr[c / 2] = make_float2(ex2(e0.x), ex2(e0.y));
+          pr[c / 2 + 1] = make_float2(ex2(e1.x), ex2(e1.y));
         }
-        const float2 e0 = ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-                                scale2, l0);
-        const float2 e1 = ffma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
-                                scale2, l1);
-        pr[c / 2] = make_float2(ex2(e0.x), ex2(e0.y));
-        pr[c / 2 + 1] = make_float2(ex2(e1.x), ex2(e1.y));
-      }
-      if (kKeys) {
-        uint32_t pk[32];
+        if (kKeys) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = pack2(pr[c].x, pr[c].y);
-        tmem_st32(t_s, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(next1);
+          for (int i = 0; i < 16; ++i) pk[i] = pack2(pr[part * 16 + i].x, pr[part * 16 + i].y);
+          tmem_st16(t_s + part * 64 + half * 16, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(part == 0 ? bar(B_PHALF) : next1);
+        }
       }
-      ok = mbar_wait(bar(B_DPFULL), j & 1, ab, deadline, p.status);
+      ok = mbar_wait(bar(B_DPFULL + (j & 1)), (j >> 1) & 1, ab, deadline,
+                     p.status);
       if (kKeys)                                     // (open likewise; for delta)
-        ok = ok && mbar_wait(bar(B_GATE2 + j % kY2), (j / kY2) & 1, ab, deadline, p.status);
-      if (!__all_sync(~0u, ok)) { ok = false; break; }
+        ok = ok && mbar_wait(bar(B_GATE2 + (j & 1)), (j >> 1) & 1, ab, deadline, p.status);
+      __syncwarp();
       tc_fence_after();
-      const uint32_t t_dp = tmem + lane_off + kColDP + half * 64;
-      tmem_ld32(t_dp, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-      tmem_ld32(t_dp + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+      const uint32_t t_dp = tmem + lane_off + kColDP + (kKeys ? 0 : (j & 1) * 128);
+      tmem_ld32(t_dp + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+      tmem_ld32(t_dp + 64 + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
       tmem_wait_ld();
       // rows of the streamed tile that are not live (queries side): their keys' columns
       uint32_t mask[2] = {~0u, ~0u};
       if (!kKeys && (list[j] & 0x8000)) {
-        const int lo = (list[j] & 0x7FFF) * BM + half * 64;
+        const int lo = (list[j] & 0x7FFF) * BM + half * 32;
         for (int s2 = 0; s2 <= p.n_slots; ++s2) {
           if (s2 < p.n_slots && ((vm >> s2) & 1u)) continue;
           const int a = (s2 < p.n_slots ? p.slot_start[s2] : p.T) - lo;
-          const int e = s2 < p.n_slots ? p.slot_start[s2 + 1] - lo : 64;
+          const int e = s2 < p.n_slots ? p.slot_start[s2 + 1] - lo : 128;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const int cl = max(a, w * 32), ch = min(e, w * 32 + 32);
+            const int cl = max(a, w * 64), ch = min(e, w * 64 + 32);
             if (cl < ch)
-              mask[w] &= ~((ch - cl == 32 ? ~0u : ((1u << (ch - cl)) - 1u)) << (cl - w * 32));
+              mask[w] &= ~((ch - cl == 32 ? ~0u : ((1u << (ch - cl)) - 1u)) << (cl - w * 64));
           }
         }
       }
-      const uint32_t stat2 = sb + SM::kStat + (kY1 + j % kY2) * (BM * 4) + half * 256;
+      const uint32_t stat2 = sb + SM::kStat + (kY1 + (j & 1)) * (BM * 4) + half * 128;
       uint32_t pk[32];
 #pragma unroll
       for (int c = 0; c < 64; c += 4) {
         float2 d0 = ndelta, d1 = ndelta;
         if (kKeys) {
-          const float4 d = lds4(stat2 + c * 4);
+          const float4 d = lds4(stat2 + (c >> 5) * 256 + (c & 31) * 4);
           d0 = make_float2(d.x, d.y);
           d1 = make_float2(d.z, d.w);
         }
@@ -605,10 +682,12 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
           pk[c] &= ((b & 1u) ? 0xFFFFu : 0u) | ((b & 2u) ? 0xFFFF0000u : 0u);
         }
       }
-      tmem_st32(t_dp, pk);
+      if (!named_bar_and(2 + (warp & 3), 64, ok)) { ok = false; break; }
+      tmem_st16(t_dp + half * 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
+      tmem_st16(t_dp + 64 + half * 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(next2);
+      mbar_arrive(done2);
     }
     // the rows' gradients: each half of the warps writes its half of the elements
     bool have = false;
@@ -658,9 +737,10 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (warp == kProducerWarp && lane == 0 && n > 0) {
       drain_wait(bar(B_A), 0);
       if (tail->tab) drain_wait(bar(B_TAB), 0);
+      // (no arrival is missing once every role has given up, so these may also run their time)
       for (int i = max(0, tail->y1 - kY1); i < tail->y1; ++i)
         drain_wait(bar(B_GATE1 + i % kY1), (i / kY1) & 1);
-      for (int i = max(0, tail->y2 - kY2); i < tail->y2; ++i)
+      for (int i = max(0, tail->y2 - kY2); kKeys && i < tail->y2; ++i)
         drain_wait(bar(B_GATE2 + i % kY2), (i / kY2) & 1);
     }
     if (warp == kMmaWarp && lane == 0) {
