@@ -207,6 +207,34 @@ struct Tail {                              // what follows the barriers in share
   int n_live, y1, y2, tab;                 // live tiles; tiles sent (for the drain)
 };
 
+// 2^x for a pair, as in the forward: by Cody-Waite range reduction (x = n + f, n the nearest integer, taken with the
+// 1.5 * 2^23 rounding constant, f in [-1/2, 1/2]) and a degree-3 polynomial minimising the
+// relative error of 2^f on [-1/2, 1/2] (Remez exchange; pose_retrieved_kv_b200/exp2_poly.py
+// derives the coefficients; relative error below 1.5e-4 in float32, far under the bf16
+// rounding of P that follows).  2^n is added to the exponent field of p(f); x is clamped below
+// at -125 so that field stays positive (2^-125 instead of ~0 is negligible next to the row sum).
+__device__ __forceinline__ float2 exp2_poly2(float2 x) {
+  constexpr float kMagic = 12582912.0f;                // 1.5 * 2^23
+  x.x = fmaxf(x.x, -125.0f);
+  x.y = fmaxf(x.y, -125.0f);
+  const float2 t = fadd2(x, make_float2(kMagic, kMagic));
+  const float2 r = fadd2(t, make_float2(-kMagic, -kMagic));      // round(x), exact
+  const float2 f = ffma2(r, make_float2(-1.0f, -1.0f), x);       // x - round(x), exact
+  float2 q = ffma2(make_float2(0.0551716685295105f, 0.0551716685295105f), f,
+                   make_float2(0.2426111251115799f, 0.2426111251115799f));
+  q = ffma2(q, f, make_float2(0.6932609677314758f, 0.6932609677314758f));
+  q = ffma2(q, f, make_float2(0.9999280571937561f, 0.9999280571937561f));
+  // exponent: the low bits of t hold n; (bits(t) << 23) mod 2^32 = n << 23
+  return make_float2(__uint_as_float(__float_as_uint(q.x) + __float_as_uint(t.x) * 8388608u),
+                     __uint_as_float(__float_as_uint(q.y) + __float_as_uint(t.y) * 8388608u));
+}
+
+// Pairs of columns (of every 8) whose exponentials run on the FMA pipe, queries side.
+#ifndef PRSINK_BWD_POLY
+#define PRSINK_BWD_POLY 0x00
+#endif
+constexpr uint32_t kPoly = PRSINK_BWD_POLY;
+
 // D (+)= A B over 64 streamed rows: A as bf16 pairs in tensor memory (8 columns per 16 rows), B
 // MN-major in shared memory (2 KB per 16 rows).
 __device__ __forceinline__ void umma_sum64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -288,12 +316,12 @@ __device__ __forceinline__ void stage_row(uint32_t taddr, uint32_t dst, int t, i
                                           uint32_t tab0, uint32_t tab1, float scale) {
   constexpr int W = D / 2;
 #pragma unroll 1
-  for (int c = 0; c < W; c += 16) {
-    uint32_t a[16];
-    tmem_ld16(taddr + c, a);
+  for (int c = 0; c < W; c += 32) {
+    uint32_t a[32];
+    tmem_ld32(taddr + c, a);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; i += 8) {
+    for (int i = 0; i < 32; i += 8) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
@@ -357,7 +385,13 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       return;
     }
   }
-  if (threadIdx.x == 0) {
+  // rows r.. of the rotated queries, the keys, the values (head-major) or d_out (token-major)
+  auto load = [&](int which, uint32_t dst, uint32_t b, int r) {
+    const CUtensorMap* tm = which == 0 ? &tm_q : which == 1 ? &tm_k : which == 2 ? &tm_v : &tm_g;
+    for (int pp = 0; pp < D / 64; ++pp)
+      tma_load_3d(dst + pp * 16384, tm, b, pp * 64, which == 3 ? h : r, which == 3 ? r : h);
+  };
+  if (threadIdx.x == kProducerWarp * 32) {
     mbar_init(bar(B_A), 1);
     for (int i = 0; i < kY1; ++i) mbar_init(bar(B_GATE1 + i), 257);
     for (int i = 0; i < kY2; ++i) {
@@ -372,6 +406,10 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     tail->ab.flag = 0;
     tail->y1 = tail->y2 = tail->tab = 0;
     fence_barrier_init();
+    // the CTA's own rows need nothing else
+    mbar_arrive_expect_tx(bar(B_A), 2 * SM::kTile);
+    load(kKeys ? 1 : 0, sb + SM::kA1, bar(B_A), row0);
+    load(kKeys ? 2 : 3, sb + SM::kA2, bar(B_A), row0);
   }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&tail->tmem), 512);
@@ -400,17 +438,8 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   const uint64_t deadline = globaltimer() + p.timeout_ns;
 
   if (warp == kProducerWarp) {
+    if (lane == 0 && n == 0) mbar_wait(bar(B_A), 0, ab, deadline, p.status);   // (no reader)
     if (lane == 0 && n > 0) {
-      // rows r.. of the rotated queries, the keys and values (head-major) or d_out (token-major)
-      auto load = [&](int which, uint32_t dst, uint32_t b, int r) {
-        const CUtensorMap* tm = which == 0 ? &tm_q : which == 1 ? &tm_k : which == 2 ? &tm_v : &tm_g;
-        for (int pp = 0; pp < D / 64; ++pp)
-          tma_load_3d(dst + pp * 16384, tm, b, pp * 64, which == 3 ? h : r,
-                      which == 3 ? r : h);
-      };
-      mbar_arrive_expect_tx(bar(B_A), 2 * SM::kTile);
-      load(kKeys ? 1 : 0, sb + SM::kA1, bar(B_A), row0);
-      load(kKeys ? 2 : 3, sb + SM::kA2, bar(B_A), row0);
       constexpr uint32_t stat = kKeys ? BM * 4 : 0;
       const float* nlse = p.nlse + static_cast<size_t>(h) * p.L_pad;
       const float* ndelta = p.ndelta + static_cast<size_t>(h) * p.L_pad;
@@ -618,8 +647,10 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                                   scale2, l0);
           const float2 e1 = ffma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
                                   scale2, l1);
-          pr[c / 2] = make_float2(ex2(e0.x), ex2(e0.y));
-          pr[c / 2 + 1] = make_float2(ex2(e1.x), ex2(e1.y));
+          pr[c / 2] = !kKeys && (kPoly >> (c / 2 & 7)) & 1u ? exp2_poly2(e0)
+                                                            : make_float2(ex2(e0.x), ex2(e0.y));
+          pr[c / 2 + 1] = !kKeys && (kPoly >> (c / 2 + 1 & 7)) & 1u
+                              ? exp2_poly2(e1) : make_float2(ex2(e1.x), ex2(e1.y));
         }
         if (kKeys) {
           uint32_t pk[16];
@@ -708,25 +739,40 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         stage_row<D>(tmem + lane_off + kColDV + half * (D / 2), stage[1], t, half * (D / 2), 0, 0,
                      1.f);
     }
-    have = named_bar_and(1, 256, have);
-    constexpr int C = D / 8;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < BM * C; i += 256) {
-      const int r = i / C, k = i % C, gr = row0 + r;
-      if (gr >= (kKeys ? p.T : p.L_blk)) continue;
-      const uint32_t off = (k >> 3) * 16384 + r * 128 + (((k & 7) ^ (r & 7)) << 4);
-      const uint4 none = make_uint4(0, 0, 0, 0);
+    // what becomes of the tile's rows: 0 nothing, 1 zeros, 2 the staged row (the statistics or
+    // the tile list that lay here are done with)
+    named_bar_sync(1, 256);
+    uint8_t* fate = smem + SM::kStat;
+    if (threadIdx.x < BM) {
+      int f = row < p.L_blk ? 2 : 0;
       if (kKeys) {
-        const int s2 = slot_of(gr, p);
-        if (!((p.grad_mask >> s2) & 1u)) continue;
-        const bool keep = have && ((vm >> s2) & 1u);
-        const size_t at = (static_cast<size_t>(h) * p.T + gr) * C + k;
-        reinterpret_cast<uint4*>(p.dk)[at] = keep ? lds4u(stage[0] + off) : none;
-        reinterpret_cast<uint4*>(p.dv)[at] = keep ? lds4u(stage[1] + off) : none;
-      } else {
-        reinterpret_cast<uint4*>(p.dq)[(static_cast<size_t>(gr) * p.H + h) * C + k] =
-            have ? lds4u(stage[0] + off) : none;
+        f = 0;
+        if (row < p.T) {
+          const int slot = slot_of(row, p);
+          if ((p.grad_mask >> slot) & 1u) f = (vm >> slot) & 1u ? 2 : 1;
+        }
       }
+      fate[t] = static_cast<uint8_t>(f);
+    }
+    have = named_bar_and(1, 256, have);
+    constexpr int C = D / 8, kPasses = BM * C / 256;
+    const int k = threadIdx.x % C, r0 = threadIdx.x / C;
+    const uint32_t off0 = (k >> 3) * 16384 + ((k & 7) << 4);
+    uint4* d1 = reinterpret_cast<uint4*>(kKeys ? p.dk : p.dq) +
+                (kKeys ? static_cast<size_t>(h) * p.T + row0
+                       : static_cast<size_t>(row0) * p.H + h) * C + k;
+    uint4* d2 = reinterpret_cast<uint4*>(p.dv) + (static_cast<size_t>(h) * p.T + row0) * C + k;
+    const size_t pitch = static_cast<size_t>(kKeys ? 1 : p.H) * C;
+#pragma unroll 4
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = r0 + i * (256 / C);
+      const int f = fate[r];
+      if (f == 0) continue;
+      const bool keep = have && f == 2;
+      const uint32_t off = (off0 ^ ((r & 7) << 4)) + r * 128;
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      d1[r * pitch] = keep ? lds4u(stage[0] + off) : none;
+      if (kKeys) d2[r * pitch] = keep ? lds4u(stage[1] + off) : none;
     }
   }
 
@@ -734,7 +780,7 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   __syncthreads();
   if (ab->flag) {
     // a wait gave up: copies and MMAs in flight end before their memory is released
-    if (warp == kProducerWarp && lane == 0 && n > 0) {
+    if (warp == kProducerWarp && lane == 0) {
       drain_wait(bar(B_A), 0);
       if (tail->tab) drain_wait(bar(B_TAB), 0);
       // (no arrival is missing once every role has given up, so these may also run their time)
