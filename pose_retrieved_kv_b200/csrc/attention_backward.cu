@@ -23,6 +23,7 @@ struct Params {
   int slot_start[kMaxSlots + 1];
   int slot_frame[kMaxSlots];
   unsigned valid_mask, grad_mask;
+  int prep_heads;                          // heads of a CTA of the preparation
   int q_row;                               // first row of the current block's ring slot
   int rope_mode;
   int rd[3];                               // rotated pairs per axis
@@ -37,6 +38,7 @@ struct Params {
   const long long* dyn_src;
   int* status;
   unsigned long long timeout_ns;
+  int debug_stall;                         // self-test: withhold the first commit of S
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
@@ -71,81 +73,90 @@ __device__ __forceinline__ float2 turn(float x0, float x1, float2 cs, float dir)
   return make_float2(x0 * cs.x - x1 * s, x0 * s + x1 * cs.x);
 }
 
-// Keys rotated into k_rot (rows of empty slots zeroed: dS is 0 there, but 0 * NaN is not) and
-// the table of the rows' cos / sin.  A CTA takes 256 / C rows, a thread one 16-byte chunk of a
-// row, whose four f64 angles serve every head.
+// Keys rotated into k_rot (rows of empty slots zeroed: dS is 0 there, but 0 * NaN is not), the
+// table of their cos / sin, queries rotated into q_rot (head-major) and the queries' statistics.
+// HBM-bound.  A CTA takes 256 / C rows and prep_heads heads, a thread one 16-byte chunk of a row,
+// whose four f64 angles serve all of them.
 template <int D>
-__global__ void __launch_bounds__(256) prep_keys_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ Params p) {
   constexpr int C = D / 8, R = 256 / C;
-  const int c = threadIdx.x % C, row = blockIdx.x * R + threadIdx.x / C;
-  if (row >= p.T) return;
-  const int s = slot_of(row, p), u = row - p.slot_start[s];
-  const bool live = (live_mask(p) >> s) & 1u;
-  const int frame = p.slot_frame[s] + u / p.L_f, tok = u % p.L_f;
+  const int c = threadIdx.x % C;
+  const int key_blocks = (p.T + R - 1) / R;
+  const bool keys = static_cast<int>(blockIdx.x) < key_blocks;
+  const int i = (keys ? blockIdx.x : blockIdx.x - key_blocks) * R + threadIdx.x / C;
+  const int h0 = blockIdx.y * p.prep_heads, h1 = min(p.H, h0 + p.prep_heads);
+  const int row = keys ? i : p.q_row + i;    // the queries sit on the current block's positions
+  const bool in = keys ? i < p.T : i < p.L_blk;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  bool live = false;
   float2 cs[4];
+  if (in) {
+    const int s = slot_of(row, p), u = row - p.slot_start[s];
+    live = !keys || ((live_mask(p) >> s) & 1u);
+    const int frame = p.slot_frame[s] + u / p.L_f, tok = u % p.L_f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = 4 * c + i;
-    int x;
-    if (p.rope_mode == 3)
-      x = j < p.rd[0] ? frame : (j < p.rd[0] + p.rd[1] ? tok / p.grid_w : tok % p.grid_w);
-    else
-      x = frame * p.L_f + tok;
-    double sn, co;
-    sincospi(static_cast<double>(x) * p.inv_pi_freq[j], &sn, &co);
-    cs[i] = make_float2(static_cast<float>(co), static_cast<float>(sn));
-    p.tab[static_cast<size_t>(row) * (D / 2) + j] = cs[i];
-  }
-  const size_t step = static_cast<size_t>(p.T) * C;
-  const size_t at = static_cast<size_t>(row) * C + c;
-#pragma unroll 4
-  for (int h = 0; h < p.H; ++h) {
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (live) {
-      x = reinterpret_cast<const uint4*>(p.k)[at + h * step];
-      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 y = turn(lo16(w[i]), hi16(w[i]), cs[i], 1.f);
-        w[i] = pack2(y.x, y.y);
-      }
+    for (int e = 0; e < 4; ++e) {
+      const int j = 4 * c + e;
+      int x;
+      if (p.rope_mode == 3)
+        x = j < p.rd[0] ? frame : (j < p.rd[0] + p.rd[1] ? tok / p.grid_w : tok % p.grid_w);
+      else
+        x = frame * p.L_f + tok;
+      double sn, co;
+      sincospi(static_cast<double>(x) * p.inv_pi_freq[j], &sn, &co);
+      cs[e] = make_float2(static_cast<float>(co), static_cast<float>(sn));
+      if (keys && blockIdx.y == 0) p.tab[static_cast<size_t>(row) * (D / 2) + j] = cs[e];
     }
-    reinterpret_cast<uint4*>(p.k_rot)[at + h * step] = x;
   }
-}
-
-// Queries rotated into q_rot (head-major) and the rows' statistics.  C threads per row.
-template <int D>
-__global__ void __launch_bounds__(256) prep_queries_kernel(const __grid_constant__ Params p) {
-  constexpr int C = D / 8, R = 256 / C;
-  const int c = threadIdx.x % C, i = blockIdx.x * R + threadIdx.x / C, h = blockIdx.y;
-  float dot = 0.f;
-  if (i < p.L_blk) {
-    const size_t at = (static_cast<size_t>(i) * p.H + h) * C + c;
-    uint4 x = reinterpret_cast<const uint4*>(p.q)[at];
-    const uint4 o = reinterpret_cast<const uint4*>(p.out)[at];
-    const uint4 g = reinterpret_cast<const uint4*>(p.d_out)[at];
+  auto rotate = [&](uint4& x) {
     uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-    const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
-    const float2* cs = p.tab + static_cast<size_t>(p.q_row + i) * (D / 2) + 4 * c;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 y = turn(lo16(w[e]), hi16(w[e]), cs[e], 1.f);
       w[e] = pack2(y.x, y.y);
-      dot += lo16(ow[e]) * lo16(gw[e]) + hi16(ow[e]) * hi16(gw[e]);
     }
-    reinterpret_cast<uint4*>(p.q_rot)[(static_cast<size_t>(h) * p.L_blk + i) * C + c] = x;
+  };
+  if (keys) {
+    if (!in) return;
+    const size_t step = static_cast<size_t>(p.T) * C;
+    const size_t at = static_cast<size_t>(row) * C + c;
+#pragma unroll 5
+    for (int h = h0; h < h1; ++h) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (live) {
+        x = __ldcs(reinterpret_cast<const uint4*>(p.k) + at + h * step);
+        rotate(x);
+      }
+      reinterpret_cast<uint4*>(p.k_rot)[at + h * step] = x;
+    }
+    return;
   }
+#pragma unroll 2
+  for (int h = h0; h < h1; ++h) {
+    float dot = 0.f;
+    if (in) {
+      const size_t at = (static_cast<size_t>(i) * p.H + h) * C + c;
+      uint4 x = reinterpret_cast<const uint4*>(p.q)[at];
+      const uint4 o = reinterpret_cast<const uint4*>(p.out)[at];
+      const uint4 g = reinterpret_cast<const uint4*>(p.d_out)[at];
+      const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-  for (int o = C / 2; o; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-  if (c == 0 && i < p.L_pad) {
-    float l = -INFINITY;                             // padding, or a row without keys
-    if (i < p.L_blk) {
-      l = p.lse[static_cast<size_t>(h) * p.L_blk + i] * -1.4426950408889634f;
-      if (l == INFINITY) l = -INFINITY;
+      for (int e = 0; e < 4; ++e) dot += lo16(ow[e]) * lo16(gw[e]) + hi16(ow[e]) * hi16(gw[e]);
+      rotate(x);
+      reinterpret_cast<uint4*>(p.q_rot)[(static_cast<size_t>(h) * p.L_blk + i) * C + c] = x;
     }
-    p.nlse[static_cast<size_t>(h) * p.L_pad + i] = l;
-    p.ndelta[static_cast<size_t>(h) * p.L_pad + i] = -dot;
+#pragma unroll
+    for (int o = C / 2; o; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+    if (c == 0 && i < p.L_pad) {
+      float l = -INFINITY;                             // padding, or a row without keys
+      if (in) {
+        l = p.lse[static_cast<size_t>(h) * p.L_blk + i] * -1.4426950408889634f;
+        if (l == INFINITY) l = -INFINITY;
+      }
+      p.nlse[static_cast<size_t>(h) * p.L_pad + i] = l;
+      p.ndelta[static_cast<size_t>(h) * p.L_pad + i] = -dot;
+    }
   }
 }
 
@@ -206,34 +217,6 @@ struct Tail {                              // what follows the barriers in share
   AbortState ab;
   int n_live, y1, y2, tab;                 // live tiles; tiles sent (for the drain)
 };
-
-// 2^x for a pair, as in the forward: by Cody-Waite range reduction (x = n + f, n the nearest integer, taken with the
-// 1.5 * 2^23 rounding constant, f in [-1/2, 1/2]) and a degree-3 polynomial minimising the
-// relative error of 2^f on [-1/2, 1/2] (Remez exchange; pose_retrieved_kv_b200/exp2_poly.py
-// derives the coefficients; relative error below 1.5e-4 in float32, far under the bf16
-// rounding of P that follows).  2^n is added to the exponent field of p(f); x is clamped below
-// at -125 so that field stays positive (2^-125 instead of ~0 is negligible next to the row sum).
-__device__ __forceinline__ float2 exp2_poly2(float2 x) {
-  constexpr float kMagic = 12582912.0f;                // 1.5 * 2^23
-  x.x = fmaxf(x.x, -125.0f);
-  x.y = fmaxf(x.y, -125.0f);
-  const float2 t = fadd2(x, make_float2(kMagic, kMagic));
-  const float2 r = fadd2(t, make_float2(-kMagic, -kMagic));      // round(x), exact
-  const float2 f = ffma2(r, make_float2(-1.0f, -1.0f), x);       // x - round(x), exact
-  float2 q = ffma2(make_float2(0.0551716685295105f, 0.0551716685295105f), f,
-                   make_float2(0.2426111251115799f, 0.2426111251115799f));
-  q = ffma2(q, f, make_float2(0.6932609677314758f, 0.6932609677314758f));
-  q = ffma2(q, f, make_float2(0.9999280571937561f, 0.9999280571937561f));
-  // exponent: the low bits of t hold n; (bits(t) << 23) mod 2^32 = n << 23
-  return make_float2(__uint_as_float(__float_as_uint(q.x) + __float_as_uint(t.x) * 8388608u),
-                     __uint_as_float(__float_as_uint(q.y) + __float_as_uint(t.y) * 8388608u));
-}
-
-// Pairs of columns (of every 8) whose exponentials run on the FMA pipe, queries side.
-#ifndef PRSINK_BWD_POLY
-#define PRSINK_BWD_POLY 0x00
-#endif
-constexpr uint32_t kPoly = PRSINK_BWD_POLY;
 
 // D (+)= A B over 64 streamed rows: A as bf16 pairs in tensor memory (8 columns per 16 rows), B
 // MN-major in shared memory (2 KB per 16 rows).
@@ -349,18 +332,18 @@ __device__ __forceinline__ void stage_row(uint32_t taddr, uint32_t dst, int t, i
   }
 }
 
+// One CTA's rows: tile `tile` of head h.
 template <int D, bool kKeys>
-__global__ void __launch_bounds__(kThreads, 1)
-products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
-                const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ Params p) {
+__device__ __forceinline__ void run_rows(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                         const CUtensorMap& tm_v, const CUtensorMap& tm_g,
+                                         const CUtensorMap& tm_t, const Params& p, int h,
+                                         int tile, uint8_t* smem) {
   using SM = Smem<D>;
   constexpr uint32_t kColS = 0, kColDP = 128;
   constexpr uint32_t kColDV = 256, kColSum = kKeys ? 256 + D : 384;
-  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, row0 = blockIdx.x * BM;
+  const int row0 = tile * BM;
   auto bar = [&](int i) { return sb + SM::kBars + i * 8; };
   auto tab_stage = [&](int j) { return sb + SM::kStage1 + (j % kY1) * SM::kTile; };
   Tail* tail = reinterpret_cast<Tail*>(smem + SM::kBars + B_COUNT * 8);
@@ -373,8 +356,8 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 
   if (kKeys) {
     // key rows that need no gradient, or get zeros
-    if (!(tile_flags(blockIdx.x, p.grad_mask, p) & 1)) return;
-    if (!(tile_flags(blockIdx.x, vm, p) & 1)) {
+    if (!(tile_flags(tile, p.grad_mask, p) & 1)) return;
+    if (!(tile_flags(tile, vm, p) & 1)) {
       for (int i = threadIdx.x; i < BM * (D / 8); i += kThreads) {
         const int r = row0 + i / (D / 8);
         if (r >= p.T || !((p.grad_mask >> slot_of(r, p)) & 1u)) continue;
@@ -531,7 +514,7 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       };
       auto score = [&](int j) {
         product<D>(tmem + kColS, a1, k1 + s1 * step);
-        umma_commit(bar(B_SFULL + (kKeys ? 0 : j & 1)));
+        if (!(p.debug_stall && j == 0)) umma_commit(bar(B_SFULL + (kKeys ? 0 : j & 1)));
       };
       auto dprob = [&](int j) {
         product<D>(tmem + kColDP + (kKeys ? 0 : (j & 1) * 128), a2, k2 + (j & 1) * step);
@@ -647,10 +630,8 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                                   scale2, l0);
           const float2 e1 = ffma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
                                   scale2, l1);
-          pr[c / 2] = !kKeys && (kPoly >> (c / 2 & 7)) & 1u ? exp2_poly2(e0)
-                                                            : make_float2(ex2(e0.x), ex2(e0.y));
-          pr[c / 2 + 1] = !kKeys && (kPoly >> (c / 2 + 1 & 7)) & 1u
-                              ? exp2_poly2(e1) : make_float2(ex2(e1.x), ex2(e1.y));
+          pr[c / 2] = make_float2(ex2(e0.x), ex2(e0.y));
+          pr[c / 2 + 1] = make_float2(ex2(e1.x), ex2(e1.y));
         }
         if (kKeys) {
           uint32_t pk[16];
@@ -802,6 +783,26 @@ products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   }
 }
 
+// Both sides in one grid: the queries' CTAs, which run longest, first, the keys' behind them, so
+// that neither side leaves SMs idle while the other could run.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+products_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
+                const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int q_tiles = p.L_pad / BM, n_q = q_tiles * p.H, b = blockIdx.x;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (b < n_q) {
+    run_rows<D, false>(tm_q, tm_k, tm_v, tm_g, tm_t, p, b / q_tiles, b % q_tiles, smem);
+  } else {
+    const int k_tiles = (p.T + BM - 1) / BM;
+    run_rows<D, true>(tm_q, tm_k, tm_v, tm_g, tm_t, p, (b - n_q) / k_tiles, (b - n_q) % k_tiles,
+                      smem);
+  }
+}
+
 // ---------------------------------------------------------------------------------- host side
 struct Plan {                              // scratch regions, each 256-byte aligned
   size_t k_rot, q_rot, tab, nlse, ndelta, total;
@@ -855,29 +856,8 @@ static void fill(const prsink_layout* L, const Geometry& g, Params& p) {
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
 }
 
-template <int D, bool kKeys>
-static int launch_products(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                           const CUtensorMap& mg, const CUtensorMap& mt, const Params& p,
-                           cudaStream_t st) {
-  const char* what = "prsink_attention_backward";
-  static bool allowed[64] = {false};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !allowed[dev]) {
-    if (cudaFuncSetAttribute(products_kernel<D, kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Smem<D>::kBytes) != cudaSuccess)
-      return check_launch(what);
-    if (dev >= 0 && dev < 64) allowed[dev] = true;
-  }
-  const int rows = kKeys ? p.T : p.L_blk;
-  products_kernel<D, kKeys><<<dim3((rows + BM - 1) / BM, p.H), kThreads, Smem<D>::kBytes, st>>>(
-      mq, mk, mv, mg, mt, p);
-  count_launch();
-  return check_launch(what);
-}
-
 template <int D>
-static int launch(const Params& p, cudaStream_t st) {
+static int launch(Params& p, cudaStream_t st) {
   constexpr int R = 256 / (D / 8);
   const char* what = "prsink_attention_backward";
   CUtensorMap mq, mk, mv, mg, mt;
@@ -889,13 +869,27 @@ static int launch(const Params& p, cudaStream_t st) {
   // the table of cos / sin as rows of 4 D bytes
   if (!rc) rc = make_map(&mt, p.tab, 2 * D, p.T, 1, 2 * row, 2 * row * p.T, BM, 1);
   if (rc) return rc;
-  prep_keys_kernel<D><<<(p.T + R - 1) / R, 256, 0, st>>>(p);
-  prep_queries_kernel<D><<<dim3(p.L_pad / R, p.H), 256, 0, st>>>(p);
+  static bool allowed[64] = {false};
+  int n_sm = 148, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (dev < 0 || dev >= 64 || !allowed[dev]) {
+    if (cudaFuncSetAttribute(products_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem<D>::kBytes) != cudaSuccess)
+      return check_launch(what);
+    if (dev >= 0 && dev < 64) allowed[dev] = true;
+  }
+  // as many heads per CTA (the angles are computed once for them) as leave eight CTAs per SM
+  const int row_ctas = (p.T + R - 1) / R + p.L_pad / R;
+  const long long most = static_cast<long long>(row_ctas) * p.H / (8 * n_sm);
+  const int groups = most < 1 ? p.H : (p.H + static_cast<int>(most) - 1) / static_cast<int>(most);
+  p.prep_heads = (p.H + groups - 1) / groups;
+  launch_dependent(prep_kernel<D>, dim3(row_ctas, groups), 256, 0, st, p);
+  const int tiles = p.L_pad / BM + (p.grad_mask ? (p.T + BM - 1) / BM : 0);
+  launch_dependent(products_kernel<D>, dim3(tiles * p.H), kThreads, Smem<D>::kBytes, st, mq, mk,
+                   mv, mg, mt, p);
   count_launch(2);
-  rc = check_launch(what);
-  if (!rc) rc = launch_products<D, false>(mq, mk, mv, mg, mt, p, st);
-  if (!rc && p.grad_mask) rc = launch_products<D, true>(mq, mk, mv, mg, mt, p, st);
-  return rc;
+  return check_launch(what);
 }
 
 }  // namespace bwd
@@ -975,6 +969,10 @@ extern "C" int prsink_attention_backward(const prsink_layout* layout, const void
   p.status = status_word_ptr();
   if (!p.status) return PRSINK_ERR_LAUNCH;
   p.timeout_ns = 2000000000ull;
+  if (const long long ns = take_debug_stall()) {
+    p.debug_stall = 1;
+    p.timeout_ns = static_cast<unsigned long long>(ns);
+  }
   p.nlse = reinterpret_cast<float*>(base + pl.nlse);
   p.ndelta = reinterpret_cast<float*>(base + pl.ndelta);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

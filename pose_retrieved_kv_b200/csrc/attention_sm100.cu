@@ -1401,10 +1401,9 @@ static int fill_params(const prsink_layout* layout, const Geometry& g, Params& p
   p.nqb = static_cast<int>((g.L_blk + NQ * BM - 1) / (NQ * BM));
   p.split_base = p.nqb * layout->n_heads;     // no split unless a caller plans one
   p.n_split = 1;
-  if (g_debug_stall_ns > 0) {           // armed by prsink_debug_attention_stall: one call only
+  if (const long long ns = take_debug_stall()) {
     p.debug_stall = 1;
-    p.timeout_ns = static_cast<unsigned long long>(g_debug_stall_ns);
-    g_debug_stall_ns = 0;
+    p.timeout_ns = static_cast<unsigned long long>(ns);
   }
   if (!p.status) return PRSINK_ERR_LAUNCH;
   return PRSINK_OK;
@@ -1450,6 +1449,13 @@ static int check_attention_args(const prsink_layout* layout, Geometry* g, const 
 }
 
 }  // namespace attn
+
+long long take_debug_stall() {
+  const long long ns = attn::g_debug_stall_ns;
+  attn::g_debug_stall_ns = 0;
+  return ns;
+}
+
 }  // namespace prsink
 
 using namespace prsink;

@@ -279,6 +279,7 @@ struct AttParams {
   float* part_o;                           // [CTAs][2][N][D] unnormalised partial results
   float2* part_ml;                         // [CTAs][2][N] their maximum (log2 units) and sum
   unsigned long long timeout_ns;
+  int debug_stall;                         // self-test: withhold the first commit of S
 };
 
 template <int D, int N>
@@ -709,7 +710,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
           for (int kk = 0; kk < D / 16; ++kk)
             umma_ss(tmem + sbuf * N, a + (kk >> 2) * panel + (kk & 3) * 2,
                     b + (kk >> 2) * (N * 8) + (kk & 3) * 2, SM::kIdescS, kk != 0);
-          umma_commit(bar(B_SDONE + st));
+          if (!(p.debug_stall && j == 0)) umma_commit(bar(B_SDONE + st));
           if (i + 1 == w.n) umma_commit(bar(B_QFREE + (seg & 1)));
         }
       }
@@ -1335,6 +1336,10 @@ extern "C" int prsink_paged_attention(const prsink_paged* paged, const void* q,
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.timeout_ns = 2000000000ull;
+  if (const long long ns = take_debug_stall()) {
+    p.debug_stall = 1;
+    p.timeout_ns = static_cast<unsigned long long>(ns);
+  }
   char* base = static_cast<char*>(scratch);
   p.part_ml = reinterpret_cast<float2*>(base);
   p.part_o = reinterpret_cast<float*>(base + pl.o);

@@ -18,6 +18,9 @@ void set_error(const char* fmt, ...);
 int check_launch(const char* what);          // PRSINK_OK or PRSINK_ERR_LAUNCH (+ text)
 void count_launch(int n = 1);
 int* status_word_ptr();                      // device address of the status word (per device)
+// Time limit (ns) armed by prsink_debug_attention_stall for this thread's next call, or 0; the
+// caller of this takes it.
+long long take_debug_stall();
 
 struct Geometry {                            // derived token counts of a layout
   long long L_f, L_blk, L_ref, T;

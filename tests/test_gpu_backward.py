@@ -248,3 +248,19 @@ def test_two_calls_at_once_with_their_own_scratch():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_normal():
+    need_gpu()
+    cfg = case("grid", head_dim=128)
+    q, k, v, do = inputs(cfg, 69)
+    out, lse = forward(cfg, q, k, v)
+    want = backward(cfg, q, k, v, do, out, lse)
+    assert P.prsink_sync_status() == P.PRSINK_OK
+    P.prsink_debug_attention_stall(200_000)
+    got = backward(cfg, q, k, v, do, out, lse)
+    assert P.prsink_sync_status() == P.PRSINK_ERR_TIMEOUT
+    assert not any(g.any() for g in got)
+    again = backward(cfg, q, k, v, do, out, lse)
+    assert P.prsink_sync_status() == P.PRSINK_OK
+    assert all(torch.equal(a, b) for a, b in zip(want, again))

@@ -421,3 +421,39 @@ def test_paged_and_slot_attention_agree():
                      for i in range(T - s["L_blk"], T)])
     # both round P, the rotated keys and queries and the result: 2 (u |o| + 3 u avg|v|), |v| < 5
     assert (got.float() - out.float()).abs().max().item() <= 2e-2
+
+
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 20)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_normal(d, group):
+    need_gpu()
+    pg = make(n_seqs=3, n_heads=2 * group, n_kv_heads=2, head_dim=d, n_pages=90, max_pages=40)
+    gen = torch.Generator().manual_seed(32)
+    lens = torch.tensor([600, 300, 64], dtype=torch.int32)
+    table = scattered_table(pg, gen, lens.tolist()).cuda()
+    k, v = (x.cuda() for x in pools(pg, gen))
+    q = torch.randn((3, 2 * group, d), generator=gen).bfloat16().cuda()
+    want = attend(pg, q, k, v, table, lens.cuda())
+    assert P.prsink_sync_status() == P.PRSINK_OK
+    P.prsink_debug_attention_stall(200_000)
+    attend(pg, q, k, v, table, lens.cuda())
+    assert P.prsink_sync_status() == P.PRSINK_ERR_TIMEOUT
+    again = attend(pg, q, k, v, table, lens.cuda())
+    assert P.prsink_sync_status() == P.PRSINK_OK
+    assert all(torch.equal(a, b) for a, b in zip(want, again))
+
+
+def test_not_a_number_in_an_attended_key_reaches_its_heads_only():
+    need_gpu()
+    pg = make(n_seqs=1, n_heads=4, n_kv_heads=2, n_pages=8, max_pages=6)
+    gen = torch.Generator().manual_seed(33)
+    k, v = pools(pg, gen)
+    k[3, 1, 5, 7] = float("nan")
+    v[2, 0, 1, 9] = float("inf")
+    table = torch.tensor([[0, 1, 2, 3, 4, 5]], dtype=torch.int32)
+    q = torch.randn((1, 4, 64), generator=gen).bfloat16()
+    out, lse = attend(pg, q.cuda(), k.cuda(), v.cuda(), table.cuda(),
+                      torch.tensor([90], dtype=torch.int32).cuda())
+    out, lse = out.cpu()[0], lse.cpu()[0]
+    assert torch.isnan(out[2:]).all() and torch.isnan(lse[2:]).all()
+    assert torch.isfinite(lse[:2]).all() and torch.isinf(out[:2, 9]).all()
+    assert torch.isfinite(out[:2, :9]).all() and torch.isfinite(out[:2, 10:]).all()
