@@ -360,7 +360,7 @@ int prsink_bank_update_policy(const prsink_layout* layout, const prsink_bank_pol
  *   out        bf16 [L_blk][H][d]  the forward's output
  *   lse        f32  [H][L_blk]     the forward's lse (required)
  *   d_out      bf16 [L_blk][H][d]  gradient of the output
- *   dq         bf16 [L_blk][H][d]  written
+ *   dq         bf16 [L_blk][H][d]  written (dq, dk and dv are buffers of their own)
  *   dk, dv     bf16 [H][T][d]      the rows of the slots in `grad_mask` are written, no other
  *              byte; rows of slots without data (valid_mask, dyn_src) get zeros.  Both may be
  *              NULL when grad_mask selects no slot (gradient of the queries alone).
@@ -419,7 +419,8 @@ typedef struct prsink_paged {
  *   q, q_rot      optional (both or neither): bf16 [n_tokens][n_heads][d] queries of the same
  *                 tokens (rows q_stride apart), written rotated to q_rot (contiguous; may be q
  *                 itself when q is contiguous)
- *   cu_new        int32 [n_seqs + 1] on the device, or NULL: one token per sequence
+ *   cu_new        int32 [n_seqs + 1] on the device, from 0 on, not decreasing (a row that no
+ *                 sequence holds is left out and recorded), or NULL: one token per sequence
  *                 (n_tokens = n_seqs); a sequence of length 0 is then an idle row, left alone
  * Rows from cu_new[n_seqs] on are ignored, their q_rot left as it was.  V is copied bit for bit,
  * K and q are rotated in f32 by angles reduced in f64 and rounded once (copied when rope_mode is

@@ -35,6 +35,9 @@ _NAMES = {PRSINK_ERR_ARG: "PRSINK_ERR_ARG", PRSINK_ERR_ALIGN: "PRSINK_ERR_ALIGN"
           PRSINK_ERR_UNSUPPORTED: "PRSINK_ERR_UNSUPPORTED", PRSINK_ERR_PAGE: "PRSINK_ERR_PAGE"}
 
 
+_bf16, _int32 = torch.bfloat16, torch.int32
+
+
 class PRSinkError(RuntimeError):
     def __init__(self, code: int, fn: str, msg: str):
         super().__init__(f"{fn}: {_NAMES.get(code, code)}: {msg}")
@@ -179,7 +182,7 @@ def _check(rc: int, fn: str):
 def _stream(stream) -> int:
     if stream is None:
         # (the raw handle of torch.cuda.current_stream(), without building a Stream object)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -232,11 +235,15 @@ def prsink_launch_count() -> int:
     return _lib.prsink_launch_count()
 
 
+_FourLongs = ctypes.c_longlong * 4
+
+
 def prsink_layout_tokens(layout: Layout):
-    vals = [ctypes.c_longlong() for _ in range(4)]
-    _check(_lib.prsink_layout_tokens(ctypes.byref(layout), *[ctypes.byref(v) for v in vals]),
+    vals = _FourLongs()
+    at = ctypes.addressof(vals)
+    _check(_lib.prsink_layout_tokens(ctypes.byref(layout), at, at + 8, at + 16, at + 24),
            "prsink_layout_tokens")
-    return tuple(v.value for v in vals)
+    return tuple(vals)
 
 
 def prsink_attention(layout: Layout, q, k_cache, v_cache, out, lse=None, dyn_src=None,
@@ -448,31 +455,23 @@ def prsink_attention_fused_split(layout: Layout, q, k_new, v_new, k_rot, k_cache
 
 def _dptr(t, name: str, dtype, numel, device: int) -> int:
     """``_ptr`` for a tensor that has to be on the current device (the one whose stream the call
-    is given to)."""
+    is given to).  One condition for a good tensor, the reason only when it fails: these checks
+    are a good part of a short call."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
-    if t.get_device() != device:
-        _wrong_device(t, name, device)
-    return t.data_ptr()
-
-
-def _wrong_device(t, name: str, device: int):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    try:
+        if (t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+                and (numel is None or t.numel() == numel)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _ptr(t, name, dtype, numel)
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
 def _device() -> int:
     """The current device's index (0 before CUDA is in use: no tensor is on a device then)."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
 def prsink_attention_backward_scratch_bytes(layout: Layout) -> int:
@@ -507,26 +506,28 @@ def _tokens(t, name: str, heads: int, d: int, device: int):
     fused projection's output) are fine, each row itself contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dtype is not _bf16:
+        raise TypeError(f"{name} must be {_bf16}, got {t.dtype}")
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != d:
         raise ValueError(f"{name} must be [n_tokens][{heads}][{d}], got {tuple(shape)}")
     n, stride = shape[0], t.stride()
-    if n and ((heads > 1 and stride[1] != d) or stride[2] != 1):
+    if n and ((stride[1] != d and heads > 1) or stride[2] != 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
     if t.get_device() != device:
-        _wrong_device(t, name, device)
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
     return t.data_ptr(), (stride[0] if n > 1 else heads * d), n
 
 
 def _paged_ptrs(paged: Paged, k_pages, v_pages, page_table, seq_lens, device: int):
     n_seqs = paged.n_seqs
     n = paged.n_pages * paged.n_kv_heads * paged.page_size * paged.head_dim
-    return (_dptr(k_pages, "k_pages", torch.bfloat16, n, device),
-            _dptr(v_pages, "v_pages", torch.bfloat16, n, device),
-            _dptr(page_table, "page_table", torch.int32, n_seqs * paged.max_pages, device),
-            _dptr(seq_lens, "seq_lens", torch.int32, n_seqs, device))
+    return (_dptr(k_pages, "k_pages", _bf16, n, device),
+            _dptr(v_pages, "v_pages", _bf16, n, device),
+            _dptr(page_table, "page_table", _int32, n_seqs * paged.max_pages, device),
+            _dptr(seq_lens, "seq_lens", _int32, n_seqs, device))
 
 
 def prsink_paged_append(paged: Paged, k_new, v_new, k_pages, v_pages, page_table, seq_lens,
@@ -543,12 +544,13 @@ def prsink_paged_append(paged: Paged, k_new, v_new, k_pages, v_pages, page_table
         qp, qs, nq = _tokens(q, "q", h, d, dev)
         if nq != n:
             raise ValueError(f"k_new holds {n} tokens, q {nq}")
-    rc = _lib.prsink_paged_append(
-        ctypes.byref(paged), kp, vp, ks, vs,
-        *_paged_ptrs(paged, k_pages, v_pages, page_table, seq_lens, dev), n,
-        _dptr(cu_new, "cu_new", torch.int32, paged.n_seqs + 1, dev), qp, qs,
-        _dptr(q_rot, "q_rot", torch.bfloat16, n * h * d, dev), _stream(stream))
-    _check(rc, "prsink_paged_append")
+    k, v, table, lens = _paged_ptrs(paged, k_pages, v_pages, page_table, seq_lens, dev)
+    cu = 0 if cu_new is None else _dptr(cu_new, "cu_new", _int32, paged.n_seqs + 1, dev)
+    qr = 0 if q_rot is None else _dptr(q_rot, "q_rot", _bf16, n * h * d, dev)
+    rc = _lib.prsink_paged_append(ctypes.byref(paged), kp, vp, ks, vs, k, v, table, lens, n, cu, qp,
+                                  qs, qr, _stream(stream))
+    if rc:
+        _check(rc, "prsink_paged_append")
 
 
 def prsink_paged_attention_scratch_bytes(paged: Paged) -> int:

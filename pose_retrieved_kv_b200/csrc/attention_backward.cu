@@ -844,13 +844,11 @@ static void fill(const prsink_layout* L, const Geometry& g, Params& p) {
   p.rope_mode = L->rope_mode;
   const int one[3] = {D, 0, 0};
   const int* split = L->rope_mode == 3 ? L->rope_split : one;
-  const double log2_base = std::log2(static_cast<double>(L->rope_base));
   int at = 0;
   for (int ax = 0; ax < 3; ++ax) {
     p.rd[ax] = split[ax] / 2;
-    for (int j = 0; j < p.rd[ax]; ++j)
-      p.inv_pi_freq[at++] = std::exp2(-(2.0 * j / split[ax]) * log2_base) *
-                            0.31830988618379067154;
+    rope_frequencies(L->rope_base, split[ax], p.inv_pi_freq + at);
+    at += p.rd[ax];
   }
   p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
@@ -922,6 +920,12 @@ extern "C" int prsink_attention_backward(const prsink_layout* layout, const void
       set_error("%s: null pointer", what);
       return PRSINK_ERR_ARG;
     }
+  for (int i = 5; i < n_bufs; ++i)         // a gradient in the place of an input or of another
+    for (int j = 0; j < i; ++j)
+      if (bufs[i] == bufs[j]) {
+        set_error("%s: dq, dk and dv must be buffers of their own", what);
+        return PRSINK_ERR_ARG;
+      }
   const int D = layout->head_dim;
   if (D != 64 && D != 128) {
     set_error("%s: head_dim %d not supported (64 or 128)", what, D);

@@ -237,6 +237,10 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
 // (O, m, l) each in scratch; a second kernel, launched early and waiting for the first, joins
 // them in CTA order (no counters to clear, no order that depends on timing).
 //
+// Where no row can be longer than kWholeRow tiles, a row belongs to the CTA that holds its first
+// unit and nothing is left to join: a tile more costs less than the second kernel (about 2 us on
+// the device and 2 us on the host).
+//
 // A tile holds whole pages up to 128 tokens, or up to 128 tokens of one page; one TMA box per
 // page.  Warps: 0-3 softmax, 4 and 7 send K and V, 5 issues the S products, 6 the O products (one
 // thread issues an MMA in about 45 cycles whatever its size, one warp a box in about 100).
@@ -244,6 +248,7 @@ constexpr int kTile = 128;                 // key rows of a tile = TMEM lanes
 constexpr int kAttThreads = 256;
 constexpr int kKeyWarp = 4, kScoreWarp = 5, kOutWarp = 6, kValueWarp = 7;
 constexpr int kMaxStages = 6;
+constexpr int kWholeRow = 4;
 constexpr int kMetaRing = 16;              // tiles whose bad-page bits are kept
 constexpr float kRescale = 8.0f;           // log2 units: O is rescaled when a maximum grows > 2^8
 
@@ -265,6 +270,7 @@ struct AttParams {
   Cache c;
   Divisor by_tile;                         // tokens of a tile (small pages) or of a page
   Divisor by_tiles_per_page, by_chunks;
+  bool whole_rows;                         // rows are not shared (see above)
   int group, chunks;                       // query heads per key head, N-column chunks of them
   int tile_tokens, pages_per_tile;         // of a tile when pages are smaller than a tile
   int tiles_per_page;                      // tiles of a page when pages are larger (else 0)
@@ -401,10 +407,16 @@ struct Walk {
   bool first;                              // the CTA's first segment
   __device__ __forceinline__ Walk(const AttParams& p, const Start& at, long long units)
       : left(units), s(at.s), hc(at.hc), i0(at.i0), n(0), row(p, at.len), first(true) {
-    take();
+    if (p.whole_rows && i0 > 0) {          // this row is the CTA's before
+      n = row.count - i0;
+      next(p);
+    } else {
+      take(p);
+    }
   }
-  __device__ __forceinline__ void take() {
-    n = static_cast<int>(min(left, static_cast<long long>(row.count - i0)));
+  __device__ __forceinline__ void take(const AttParams& p) {
+    n = row.count - i0;
+    if (!p.whole_rows) n = static_cast<int>(min(left, static_cast<long long>(n)));
   }
   __device__ __forceinline__ void next(const AttParams& p) {
     left -= n;
@@ -418,7 +430,7 @@ struct Walk {
         row = Row(p, seq_len(p.c, s));
       } while (row.count == 0);
     }
-    take();
+    take(p);
   }
 };
 
@@ -1074,9 +1086,11 @@ static int check(const prsink_paged* g, const char* what, Cache* c) {
     return PRSINK_ERR_ARG;
   }
   if (static_cast<long long>(g->max_pages) * g->page_size > (1ll << 30) ||
-      static_cast<long long>(g->n_pages) * g->n_kv_heads > (1ll << 30)) {
-    set_error("%s: paged cache too large (%d x %d tokens per sequence, %d pages x %d heads)", what,
-              g->max_pages, g->page_size, g->n_pages, g->n_kv_heads);
+      static_cast<long long>(g->n_pages) * g->n_kv_heads > (1ll << 30) ||
+      static_cast<long long>(g->n_seqs) * g->n_heads > (1ll << 30)) {
+    set_error("%s: paged cache too large (%d sequences x %d heads of %d x %d tokens, %d pages x %d "
+              "heads)", what, g->n_seqs, g->n_heads, g->max_pages, g->page_size, g->n_pages,
+              g->n_kv_heads);
     return PRSINK_ERR_ARG;
   }
   if (g->rope_mode != 0 && g->rope_mode != 1 && g->rope_mode != 3) {
@@ -1201,8 +1215,11 @@ static int launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const 
     if (dev >= 0 && dev < 64) allowed[dev] = true;
   }
   launch_dependent(paged_attention_kernel<D, N>, grid, kAttThreads, smem, st, mq, mk, mv, p);
-  launch_dependent(paged_join_kernel<D, N>, grid, kJoinThreads, 0, st, p);
-  count_launch(2);
+  count_launch();
+  if (!p.whole_rows) {
+    launch_dependent(paged_join_kernel<D, N>, grid, kJoinThreads, 0, st, p);
+    count_launch();
+  }
   return check_launch("prsink_paged_attention");
 }
 
@@ -1266,13 +1283,11 @@ extern "C" int prsink_paged_append(const prsink_paged* paged, const void* k_new,
   if (p.rope_mode) {
     const int one[3] = {D, 0, 0};
     const int* split = p.rope_mode == 3 ? paged->rope_split : one;
-    const double log2_base = std::log2(static_cast<double>(paged->rope_base));
     int at = 0;
     for (int ax = 0; ax < 3; ++ax) {
       p.rd[ax] = split[ax] / 2;
-      for (int j = 0; j < p.rd[ax]; ++j)
-        p.inv_pi_freq[at++] = std::exp2(-(2.0 * j / split[ax]) * log2_base) *
-                              0.31830988618379067154;
+      rope_frequencies(paged->rope_base, split[ax], p.inv_pi_freq + at);
+      at += p.rd[ax];
     }
     if (p.rope_mode == 3) {
       p.grid_w = paged->grid_w;
@@ -1329,6 +1344,19 @@ extern "C" int prsink_paged_attention(const prsink_paged* paged, const void* q,
   p.pages_per_tile = ps < kTile ? kTile / ps : 1;
   p.tile_tokens = ps < kTile ? p.pages_per_tile * ps : kTile;
   p.box_rows = ps < kTile ? ps : kTile;
+  // tiles of the longest row: the table's capacity, or the sinks and the window with the tiles
+  // that they begin and end in
+  auto tiles_of = [&](long long tokens) {
+    const long long in_pages = (tokens + ps - 1) / ps;
+    return p.tiles_per_page ? in_pages * p.tiles_per_page
+                            : (in_pages + p.pages_per_tile - 1) / p.pages_per_tile;
+  };
+  long long longest = tiles_of(p.c.capacity);
+  if (p.c.window > 0) {
+    const long long bounded = tiles_of(p.c.n_sink) + tiles_of(p.c.window) + 1;
+    if (bounded < longest) longest = bounded;
+  }
+  p.whole_rows = longest <= kWholeRow;
   p.by_tile.set(ps < kTile ? p.tile_tokens : ps);
   p.by_tiles_per_page.set(p.tiles_per_page ? p.tiles_per_page : 1);
   p.by_chunks.set(p.chunks);

@@ -4,6 +4,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -101,6 +102,18 @@ int make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_
   const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
   const cuuint32_t box[3] = {64, box1, box2};
   return encode_map(m, base, 3, dims, strides, box);
+}
+
+void rope_frequencies(double base, int dims, double* out) {
+  // powers of the ratio of neighbours, eight at a time: one exp2 per eight pairs and for the
+  // seven in between (each result is off by two roundings of f64 at most)
+  const double step = -2.0 / dims * std::log2(base);
+  double fine[8];
+  for (int k = 0; k < 8; ++k) fine[k] = std::exp2(step * k);
+  for (int j = 0; j < dims / 2; j += 8) {
+    const double coarse = std::exp2(step * j) * 0.31830988618379067154;
+    for (int k = 0; k < 8 && j + k < dims / 2; ++k) out[j + k] = coarse * fine[k];
+  }
 }
 
 int make_map_rows(CUtensorMap* m, const void* base, int D, uint64_t rows, uint64_t n_blocks,

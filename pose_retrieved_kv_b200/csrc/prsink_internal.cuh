@@ -54,6 +54,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 int make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
              uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box1, uint32_t box2);
 
+// out[j] = base^(-2j/dims) / pi for j < dims / 2: the turns (in half circles) per position of the
+// pairs of one axis.
+void rope_frequencies(double base, int dims, double* out);
+
 // 5-D bf16 map of rows of D elements in blocks (n_blocks blocks of `rows` rows, contiguous):
 // dimensions (64 elements, 8 rows, D / 64 panels, rows / 8 groups, block), box 64 x 8 x D/64 x
 // box_groups x 1.  One box lands both panels of its rows, as 1 KB swizzle atoms [group][panel].

@@ -32,7 +32,7 @@ def _attend(pg, **kw):
     dict(n_seqs=-1), dict(n_seqs=65536), dict(n_heads=0), dict(n_kv_heads=0), dict(n_heads=5),
     dict(page_size=0), dict(n_pages=0), dict(max_pages=0), dict(n_sink=-1), dict(window=-1),
     dict(rope_mode=2), dict(rope_base=0.0), dict(rope_base=float("nan")),
-    dict(max_pages=1 << 27), dict(n_pages=1 << 30),
+    dict(max_pages=1 << 27), dict(n_pages=1 << 30), dict(n_seqs=65535, n_heads=65534),
     dict(rope_mode=3, rope_split=(24, 20, 18), grid_h=4, grid_w=4),
     dict(rope_mode=3, rope_split=(23, 21, 20), grid_h=4, grid_w=4),
     dict(rope_mode=3, rope_split=(24, 20, 20), grid_h=0, grid_w=4)])
@@ -118,12 +118,14 @@ def test_backward_refusals():
 
     def call(layout=lay, scratch=256, n=nb, mask=0xFF, dyn=None, **kw):
         names = ("q", "k", "v", "out", "lse", "d_out", "dq", "dk", "dv")
-        a = [kw.get(x, 16) for x in names]
+        a = [kw.get(x, 16 * (i + 1)) for i, x in enumerate(names)]
         return lib.prsink_attention_backward(ctypes.byref(layout), *a, mask, dyn, scratch, n, None)
     for name in ("q", "k", "v", "out", "lse", "d_out", "dq", "dk", "dv"):
         assert call(**{name: None}) == P.PRSINK_ERR_ARG, name
     for name in ("q", "k", "v", "out", "d_out", "dq", "dk", "dv"):
         assert call(**{name: 24}) == P.PRSINK_ERR_ALIGN, name
+    for name, other in (("dq", 16), ("dk", 32), ("dv", 48), ("dq", 96), ("dk", 112), ("dv", 128)):
+        assert call(**{name: other}) == P.PRSINK_ERR_ARG, name        # in another's place
     assert call(lse=18) == P.PRSINK_ERR_ALIGN and call(dyn=12) == P.PRSINK_ERR_ALIGN
     assert call(scratch=None) == P.PRSINK_ERR_ARG and call(scratch=128) == P.PRSINK_ERR_ARG
     assert call(n=nb - 1) == P.PRSINK_ERR_ARG
