@@ -243,7 +243,14 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
 //
 // A tile holds whole pages up to 128 tokens, or up to 128 tokens of one page; one TMA box per
 // page.  Warps: 0-3 softmax, 4 and 7 send K and V, 5 issues the S products, 6 the O products (one
-// thread issues an MMA in about 45 cycles whatever its size, one warp a box in about 100).
+// thread issues an MMA in about 45 cycles whatever its size, one warp a box in about 100: with one
+// sending warp, pages of 8 took 402 us where two take 319, 64 sequences x 8000 tokens).
+//
+// Measured on a B200 (6551 GB/s copy): 64 sequences x 8000 tokens x 8 key heads of 128, 64 query
+// heads, 316 us (6.6 TB/s) at pages of 16 and more; 48 ragged sequences of up to 16001 tokens,
+// 40 heads on 8, pages of 16, 239 us (6.6 TB/s); one sequence of 14400 tokens, 40 heads, 52.5 us
+// (5.6 TB/s: the start, about 5 us to the first landed tile, and the join are 7 us of it).  A tile
+// takes the softmax warps about 0.5 us where HBM needs 1.45 (head_dim 128) or 0.73 (64).
 constexpr int kTile = 128;                 // key rows of a tile = TMEM lanes
 constexpr int kAttThreads = 256;
 constexpr int kKeyWarp = 4, kScoreWarp = 5, kOutWarp = 6, kValueWarp = 7;
