@@ -36,6 +36,7 @@ CASES = [
     case("grid", valid_mask=0b101010, block_index=8, head_dim=128),
     case("grid", head_dim=128, rope_split=(64, 32, 32)),
     case("grid", head_dim=128, rope_split=(0, 64, 64), n_heads=3, ref_frames=2),
+    case("grid", n_heads=24, grid_h=12, grid_w=12),        # several heads per preparing CTA
 ]
 
 

@@ -457,3 +457,87 @@ def test_not_a_number_in_an_attended_key_reaches_its_heads_only():
     assert torch.isnan(out[2:]).all() and torch.isnan(lse[2:]).all()
     assert torch.isfinite(lse[:2]).all() and torch.isinf(out[:2, 9]).all()
     assert torch.isfinite(out[:2, :9]).all() and torch.isfinite(out[:2, 10:]).all()
+
+
+def test_append_many_tokens_of_many_sequences():
+    """Enough tokens that several share a CTA, and enough sequences that the search for a token's
+    sequence takes more than one step; sequences without new tokens among them."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(41)
+    g = np.random.default_rng(41)
+    new = g.integers(0, 20, 300)
+    new[[0, 7, 8, 299]] = 0
+    new[100] = 31
+    lens = new + g.integers(0, 40, 300)
+    pg = make(n_seqs=300, n_heads=3, n_kv_heads=1, page_size=24, n_pages=1200, max_pages=3)
+    assert new.sum() > 16 * 148
+    table = scattered_table(pg, gen, lens)
+    k0, v0 = pools(pg, gen)
+    n = int(new.sum())
+    q, k, v = (torch.randn((n, h, 64), generator=gen).bfloat16() for h in (3, 1, 1))
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(new)])).int()
+    kd, vd, qr = k0.cuda(), v0.cuda(), torch.empty_like(q, device="cuda")
+    P.prsink_paged_append(P.make_paged(**pg), k.cuda(), v.cuda(), kd, vd, table.cuda(),
+                          torch.from_numpy(lens).int().cuda(), cu_new=cu.cuda(), q=q.cuda(),
+                          q_rot=qr)
+    assert P.prsink_sync_status() == P.PRSINK_OK
+    rk, rv, rq = oracle.paged_append(pg, f64(k), f64(v), f64(k0), f64(v0), table.tolist(),
+                                     lens.tolist(), cu.tolist(), f64(q), np.zeros((n, 3, 64)))
+    assert np.array_equal(f64(vd), rv)
+    assert np.all(np.abs(f64(kd) - rk) <= U * np.abs(rk) + 2.0 ** -18)
+    assert np.all(np.abs(f64(qr) - rq) <= U * np.abs(rq) + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("page,d", [(200, 128), (200, 64), (136, 128), (72, 128), (40, 64)])
+def test_attention_more_sequences_than_threads_and_odd_pages(page, d):
+    """Several sequences per thread of the scan (empty ones among them), rows shared by CTAs,
+    pages whose tiles are ragged."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(42)
+    g = np.random.default_rng(page + d)
+    lens = torch.from_numpy(g.integers(0, 260, 600)).int()
+    lens[[0, 1, 77, 598, 599]] = 0
+    lens[[5, 300]] = torch.tensor([900, 1200], dtype=torch.int32)
+    width = -(-1200 // page)
+    pages = int(sum(-(-int(n) // page) for n in lens)) + 2
+    pg = make(n_seqs=600, n_heads=3, n_kv_heads=1, head_dim=d, page_size=page, n_pages=pages,
+              max_pages=width)
+    table = scattered_table(pg, gen, lens.tolist())
+    k, v = pools(pg, gen)
+    q = torch.randn((600, 3, d), generator=gen).bfloat16()
+    out, lse = attend(pg, q.cuda(), k.cuda(), v.cuda(), table.cuda(), lens.cuda())
+    assert P.prsink_sync_status() == P.PRSINK_OK
+    check_attention(pg, out, lse, q, k, v, table, lens)
+
+
+def test_two_captured_calls_that_share_their_scratch():
+    """Two graphs with the same scratch, replayed in turn on one stream: neither depends on what
+    the other left there."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(43)
+    calls = []
+    scratch = None
+    for i, lens in enumerate(([2000, 700], [3000])):
+        pg = make(n_seqs=len(lens), n_heads=4, n_kv_heads=2, head_dim=128, n_pages=200,
+                  max_pages=190)
+        p = P.make_paged(**pg)
+        if scratch is None:
+            scratch = torch.full((P.prsink_paged_attention_scratch_bytes(p),), 255,
+                                 dtype=torch.uint8, device="cuda")
+        table = scattered_table(pg, gen, lens).cuda()
+        k, v = (x.cuda() for x in pools(pg, gen))
+        q = torch.randn((len(lens), 4, 128), generator=gen).bfloat16().cuda()
+        ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        want = attend(pg, q, k, v, table, ln)
+        out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            P.prsink_paged_attention(p, q, k, v, table, ln, out, scratch, lse=lse)
+        calls.append((graph, out, lse, want, (p, q, k, v, table, ln)))
+    for _ in range(3):
+        for graph, out, lse, want, _ in calls:
+            out.fill_(float("nan"))
+            lse.fill_(float("nan"))
+            graph.replay()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])

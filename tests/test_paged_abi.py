@@ -136,4 +136,6 @@ def test_backward_refusals():
             P.prsink_attention_backward_scratch_bytes(lay2)
     lay96 = P.make_layout(**{**synth.preset("tiny"), "head_dim": 96, "rope_split": (96, 0, 0)})
     assert call(layout=lay96) == P.PRSINK_ERR_UNSUPPORTED
+    long = P.make_layout(**{**synth.preset("tiny"), "grid_h": 100, "grid_w": 100})   # 160000 keys
+    assert call(layout=long) == P.PRSINK_ERR_UNSUPPORTED
     assert P.prsink_launch_count() == before
