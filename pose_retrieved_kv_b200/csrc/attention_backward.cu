@@ -577,13 +577,16 @@ __device__ __forceinline__ void run_rows(const CUtensorMap& tm_q, const CUtensor
     }
     __syncwarp();
   } else {
-    // Columns of a thread: 32 of the streamed rows 0-63 and 32 of 64-127 (part 0 / 1 of the row).
-    // P and dS of a part go, as bf16 pairs, into the first 32 columns of its 64; the two warps
-    // that share the lanes meet before that, since each writes where the other has read.
+    // Columns of a thread, in two parts of 32.  Keys: one of the streamed rows 0-63 and one of
+    // 64-127, so that the first half of P is ready early; P and dS go, as bf16 pairs, into the
+    // first 32 columns of each 64, and the two warps that share the lanes meet before that, since
+    // each writes where the other has read.  Queries: 64 columns of its own.
     const int half = warp >> 2;
     const int row = row0 + (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_off + kColS;
+    const uint32_t col[2] = {kKeys ? half * 32u : half * 64u, kKeys ? 64u + half * 32u : half * 64u + 32u};
+    const uint32_t packed[2] = {kKeys ? half * 16u : half * 64u, kKeys ? 64u + half * 16u : half * 64u + 16u};
     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     float2 nlse = make_float2(0.f, 0.f), ndelta = nlse;    // queries: this row's
     if (!kKeys) {
@@ -614,15 +617,16 @@ __device__ __forceinline__ void run_rows(const CUtensorMap& tm_q, const CUtensor
       __syncwarp();
       tc_fence_after();
       uint32_t s[64];
-      tmem_ld32(t_s + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-      tmem_ld32(t_s + 64 + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+      tmem_ld32(t_s + col[0], *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+      tmem_ld32(t_s + col[1], *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
       tmem_wait_ld();
       if (!kKeys) {
         tc_fence_before();
         mbar_arrive(next1);
       }
       // (a wait that gave up in one of the two warps ends the loop for both)
-      if (!named_bar_and(2 + (warp & 3), 64, ok)) { ok = false; break; }
+      ok = kKeys ? named_bar_and(2 + (warp & 3), 64, ok) : __all_sync(~0u, ok);
+      if (!ok) break;
       float2 pr[32];
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
@@ -646,7 +650,7 @@ __device__ __forceinline__ void run_rows(const CUtensorMap& tm_q, const CUtensor
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = pack2(pr[part * 16 + i].x, pr[part * 16 + i].y);
-          tmem_st16(t_s + part * 64 + half * 16, pk);
+          tmem_st16(t_s + packed[part], pk);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(part == 0 ? bar(B_PHALF) : next1);
@@ -659,22 +663,22 @@ __device__ __forceinline__ void run_rows(const CUtensorMap& tm_q, const CUtensor
       __syncwarp();
       tc_fence_after();
       const uint32_t t_dp = tmem + lane_off + kColDP + (kKeys ? 0 : (j & 1) * 128);
-      tmem_ld32(t_dp + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-      tmem_ld32(t_dp + 64 + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+      tmem_ld32(t_dp + col[0], *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+      tmem_ld32(t_dp + col[1], *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
       tmem_wait_ld();
       // rows of the streamed tile that are not live (queries side): their keys' columns
       uint32_t mask[2] = {~0u, ~0u};
       if (!kKeys && (list[j] & 0x8000)) {
-        const int lo = (list[j] & 0x7FFF) * BM + half * 32;
+        const int lo = (list[j] & 0x7FFF) * BM + half * 64;
         for (int s2 = 0; s2 <= p.n_slots; ++s2) {
           if (s2 < p.n_slots && ((vm >> s2) & 1u)) continue;
           const int a = (s2 < p.n_slots ? p.slot_start[s2] : p.T) - lo;
-          const int e = s2 < p.n_slots ? p.slot_start[s2 + 1] - lo : 128;
+          const int e = s2 < p.n_slots ? p.slot_start[s2 + 1] - lo : 64;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const int cl = max(a, w * 64), ch = min(e, w * 64 + 32);
+            const int cl = max(a, w * 32), ch = min(e, w * 32 + 32);
             if (cl < ch)
-              mask[w] &= ~((ch - cl == 32 ? ~0u : ((1u << (ch - cl)) - 1u)) << (cl - w * 64));
+              mask[w] &= ~((ch - cl == 32 ? ~0u : ((1u << (ch - cl)) - 1u)) << (cl - w * 32));
           }
         }
       }
@@ -703,9 +707,10 @@ __device__ __forceinline__ void run_rows(const CUtensorMap& tm_q, const CUtensor
           pk[c] &= ((b & 1u) ? 0xFFFFu : 0u) | ((b & 2u) ? 0xFFFF0000u : 0u);
         }
       }
-      if (!named_bar_and(2 + (warp & 3), 64, ok)) { ok = false; break; }
-      tmem_st16(t_dp + half * 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
-      tmem_st16(t_dp + 64 + half * 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
+      ok = kKeys ? named_bar_and(2 + (warp & 3), 64, ok) : __all_sync(~0u, ok);
+      if (!ok) break;
+      tmem_st16(t_dp + packed[0], *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
+      tmem_st16(t_dp + packed[1], *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(done2);
