@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ Param
 // five that one pass would need, but no sum crosses a CTA: a fused pass would have to add 64 KB
 // of float32 dQ to global memory per pair, in an order that changes from run to run.
 //
-// Warps 0-7 turn S into P and dP into dS (row = lane, a half of the streamed rows each), warp 8
+// Warps 0-7 turn S into P and dP into dS (row = lane, a half of the streamed rows each: 32 of
+// every 64 on the keys' side, 64 in one piece on the queries', see `col`), warp 8
 // sends the tiles (Y1 through three stages, since both S and the sum read it; Y2 through two),
 // warp 9 issues the MMAs:
 //   kKeys      dV(j) in two halves, S(j+1)  |  dK(j)  dP(j+1)
