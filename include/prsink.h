@@ -440,8 +440,8 @@ int prsink_paged_append(const prsink_paged* paged, const void* k_new, const void
  * i >= seq_lens[s] - window (every token when window = 0).  Pages without such a token are not
  * read and their table entries not looked at (evicted pages may hold any index).
  * The work is divided evenly over the SMs along the tokens of all sequences and heads; where a
- * (sequence, head) is shared by several CTAs, the last one to finish joins their partial results
- * in a fixed order (the same inputs give the same bits on the same device).
+ * (sequence, head) is shared by several CTAs, a second kernel joins their partial results in a
+ * fixed order (the same inputs give the same bits on the same device).
  *   q        bf16 [n_seqs][n_heads][d]   rotated queries (prsink_paged_append)
  *   out      bf16 [n_seqs][n_heads][d]   written; 0 for a sequence with nothing to attend
  *   lse      f32  [n_seqs][n_heads]      natural log-sum-exp (-inf likewise), or NULL
