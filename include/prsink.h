@@ -443,7 +443,8 @@ int prsink_paged_append(const prsink_paged* paged, const void* k_new, const void
  * (sequence, head) is shared by several CTAs, a second kernel joins their partial results in a
  * fixed order (the same inputs give the same bits on the same device).
  *   q        bf16 [n_seqs][n_heads][d]   rotated queries (prsink_paged_append)
- *   out      bf16 [n_seqs][n_heads][d]   written; 0 for a sequence with nothing to attend
+ *   out      bf16 [n_seqs][n_heads][d]   written; 0 for a sequence with nothing to attend, or with
+ *            scores of -inf alone (a score of -inf, from keys with infinities, weighs nothing)
  *   lse      f32  [n_seqs][n_heads]      natural log-sum-exp (-inf likewise), or NULL
  *   scratch  device memory of prsink_paged_attention_scratch_bytes(paged) bytes, 256-byte
  *            aligned, owned by the caller, not shared with a concurrent call

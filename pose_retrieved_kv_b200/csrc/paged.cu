@@ -258,6 +258,9 @@ constexpr int kMaxStages = 6;
 constexpr int kWholeRow = 4;
 constexpr int kMetaRing = 16;              // tiles whose bad-page bits are kept
 constexpr float kRescale = 8.0f;           // log2 units: O is rescaled when a maximum grows > 2^8
+// Offset of a head whose scores so far are all -inf.  Finite: a score of -inf stays -inf beside it
+// (it weighs nothing; -inf minus -inf would be NaN), a finite one exceeds it by far more than 2^8.
+constexpr float kNoOffset = -3.402823466e38f;
 
 // Quotient by a constant of the call: q = (n + hi(n m)) >> s for 0 <= n < 2^31, with 2^s the next
 // power of two >= d and m = floor(2^32 (2^s - d) / d) + 1.
@@ -849,9 +852,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (t < nh) {
               const float mt = fmaxf(fmaxf(red_s[0][t], red_s[1][t]),
                                      fmaxf(red_s[2][t], red_s[3][t])) * p.scale_log2;
-              m = i > 0 ? m_s[t] : -INFINITY;
-              if (m == -INFINITY || mt > m + kRescale) {
-                if (m > -INFINITY) alpha = ex2(m - mt);
+              m = i > 0 ? m_s[t] : kNoOffset;
+              if (mt > m + kRescale) {
+                if (m > kNoOffset) alpha = ex2(m - mt);
                 m = mt;
               }
             }
@@ -887,11 +890,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (g >= nh) break;
             const float4 m4 = *reinterpret_cast<const float4*>(&m_s[g]);
             const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-            // an offset of -inf: every score so far is -inf as well, and weighs nothing
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              z[g + e] = fmaf(__uint_as_float(s[g + e]), p.scale_log2,
-                              m[e] > -INFINITY ? -m[e] : 0.f);
+              z[g + e] = fmaf(__uint_as_float(s[g + e]), p.scale_log2, -m[e]);
           }
         } else if (j > 1) {
           ok = o_done(rv2);                        // its P buffer may be overwritten
@@ -1047,7 +1048,8 @@ paged_join_kernel(const __grid_constant__ AttParams p) {
       float2 ml = make_float2(-INFINITY, 0.f);
       if (i0 + lane < n) ml = __ldcg(&p.part_ml[part(i0 + lane)]);
       const float top = fmaxf(M, warp_max(ml.x));
-      // (the first batch: nothing to rescale; a batch of empty parts leaves M at -inf)
+      // (the first batch: nothing to rescale; a part without a finite score has the offset
+      // kNoOffset and sums of 0)
       const float scale = M > -INFINITY ? ex2(M - top) : 0.f;
       const float wt = ml.x > -INFINITY ? ex2(ml.x - top) : 0.f;
       M = top;

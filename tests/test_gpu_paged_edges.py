@@ -1,0 +1,39 @@
+"""GPU tests of the paged calls at their edges.
+
+Tolerances: those of ``tests/test_gpu_paged.py`` (derived there)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import pose_retrieved_kv_b200 as P
+from tests._gpu import f64, need_gpu
+from tests.test_gpu_paged import attend, bits, check_attention, make, pools, scattered_table
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,length,dead,max_pages", [(3, 480, 300, 30), (8, 8000, 5100, 501)])
+def test_scores_of_minus_infinity_weigh_nothing(d, n, length, dead, max_pages):
+    """Keys with an element of -inf (a mask folded into the keys) against queries that are positive
+    there: whole tiles of such scores at the start of a row, in rows of one CTA (n = 3) and in
+    shared ones, beside a key head without any.  One sequence holds nothing else."""
+    need_gpu()
+    pg = make(n_seqs=n, n_heads=6, n_kv_heads=2, head_dim=d, max_pages=max_pages,
+              n_pages=n * max_pages)
+    gen = torch.Generator().manual_seed(51)
+    lens = torch.tensor([length] * (n - 1) + [dead], dtype=torch.int32)
+    table = scattered_table(pg, gen, lens.tolist())
+    k, v = pools(pg, gen)
+    for s in range(n):
+        for t in range(dead):
+            k[table[s, t // 16], 0, t % 16, 5] = -float("inf")
+    q = torch.randn((n, 6, d), generator=gen).bfloat16()
+    q[..., 5] = q[..., 5].abs() + 0.5
+    out, lse = attend(pg, q.cuda(), k.cuda(), v.cuda(), table.cuda(), lens.cuda())
+    assert P.prsink_sync_status() == P.PRSINK_OK
+    assert torch.all(out[-1, :3] == 0) and torch.all(lse[-1, :3] == -float("inf"))
+    assert torch.isfinite(lse[-1, 3:]).all()
+    check_attention(dict(pg, n_seqs=n - 1), out[:-1], lse[:-1], q[:-1], k, v, table[:-1],
+                    lens[:-1])
