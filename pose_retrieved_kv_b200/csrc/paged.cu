@@ -446,7 +446,8 @@ struct Walk {
 
 __device__ __forceinline__ float warp_max(float x) {
   float y;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  // volatile: all 32 lanes have to get here, also where one lane alone uses the result
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ void sts_bf16(uint32_t addr, float x) {
