@@ -216,7 +216,12 @@ struct Smem {
   static constexpr int kStat = kStage2 + kY2 * kTile;
   static constexpr int kStatBytes = (kY1 + kY2) * BM * 4;
   static constexpr int kBars = kStat + kStatBytes;
-  static constexpr int kBytes = kBars + B_COUNT * 8 + 32;
+  static constexpr int kTail = kBars + B_COUNT * 8;
+  // what becomes of the tile's rows at the end: memory of its own, since copies of the statistics
+  // may still be on their way when a wait has given up, and a row's fate decides whether it is
+  // written (rows past the end among them)
+  static constexpr int kFate = kTail + 32;
+  static constexpr int kBytes = kFate + BM;
   static constexpr uint32_t kIdescSum = idesc_bf16_f32(128, D, false, true);
   static_assert(kMaxTiles * 2 <= kStatBytes, "tile list");
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -356,7 +361,8 @@ __device__ __forceinline__ void run_rows(const CUtensorMap& tm_q, const CUtensor
   const int row0 = tile * BM;
   auto bar = [&](int i) { return sb + SM::kBars + i * 8; };
   auto tab_stage = [&](int j) { return sb + SM::kStage1 + (j % kY1) * SM::kTile; };
-  Tail* tail = reinterpret_cast<Tail*>(smem + SM::kBars + B_COUNT * 8);
+  Tail* tail = reinterpret_cast<Tail*>(smem + SM::kTail);
+  static_assert(sizeof(Tail) <= SM::kFate - SM::kTail, "tail");
   uint16_t* list = reinterpret_cast<uint16_t*>(smem + SM::kStat);      // (queries only)
   const unsigned vm = live_mask(p);
   if (sb & 1023u) {                                  // (the swizzle needs 1 KB atoms; no static
@@ -735,10 +741,8 @@ __device__ __forceinline__ void run_rows(const CUtensorMap& tm_q, const CUtensor
         stage_row<D>(tmem + lane_off + kColDV + half * (D / 2), stage[1], t, half * (D / 2), 0, 0,
                      1.f);
     }
-    // what becomes of the tile's rows: 0 nothing, 1 zeros, 2 the staged row (the statistics or
-    // the tile list that lay here are done with)
-    named_bar_sync(1, 256);
-    uint8_t* fate = smem + SM::kStat;
+    // what becomes of the tile's rows: 0 nothing, 1 zeros, 2 the staged row
+    uint8_t* fate = smem + SM::kFate;
     if (threadIdx.x < BM) {
       int f = row < p.L_blk ? 2 : 0;
       if (kKeys) {
