@@ -783,8 +783,10 @@ __device__ __forceinline__ void run_rows(const CUtensorMap& tm_q, const CUtensor
     if (warp == kProducerWarp && lane == 0) {
       drain_wait(bar(B_A), 0);
       if (tail->tab) drain_wait(bar(B_TAB), 0);
-      // (no arrival is missing once every role has given up, so these may also run their time)
-      for (int i = max(0, tail->y1 - kY1); i < tail->y1; ++i)
+      // (arrivals may be missing once every role has given up: these then run their time, which is
+      // far more than a copy takes)
+      const int sent = kKeys ? tail->y1 : tail->y2;  // (queries: Y2 goes first, on the same gate)
+      for (int i = max(0, sent - kY1); i < sent; ++i)
         drain_wait(bar(B_GATE1 + i % kY1), (i / kY1) & 1);
       for (int i = max(0, tail->y2 - kY2); kKeys && i < tail->y2; ++i)
         drain_wait(bar(B_GATE2 + i % kY2), (i / kY2) & 1);
