@@ -18,10 +18,10 @@
  *   - Return value: PRSINK_OK (0) or a negative PRSINK_ERR_* code.  Invalid arguments are
  *     rejected on the host before anything is launched.  No C++ exception crosses the ABI.
  *   - Device-side waits are bounded.  A wait that runs out records PRSINK_ERR_TIMEOUT in a
- *     device status word; prsink_sync_status() reads and clears it.  There is ONE status word
- *     per device, shared by every stream and host thread that uses the library on it: a
- *     timeout raised by a kernel on stream A is reported (and cleared) by a
- *     prsink_sync_status() call made for stream B.  The paged calls record lengths and page
+ *     device status word; prsink_sync_status() reports and clears it, one kind of error per
+ *     call.  There is ONE status word per device, shared by every stream and host thread that
+ *     uses the library on it: a timeout raised by a kernel on stream A is reported (and
+ *     cleared) by a prsink_sync_status() call made for stream B.  The paged calls record lengths and page
  *     indices they had to refuse on the device in the same word (PRSINK_ERR_PAGE).
  *
  * Cache layout (the "slot-indexed" cache).  For one layer, K and V caches are each
@@ -457,11 +457,12 @@ int prsink_paged_attention(const prsink_paged* paged, const void* q, const void*
 /* Scratch bytes prsink_paged_attention needs on the current device (-1 for an invalid argument). */
 long long prsink_paged_attention_scratch_bytes(const prsink_paged* paged);
 
-/* Synchronise `stream`, then read and clear the status word of the current device:
- * PRSINK_OK, or PRSINK_ERR_TIMEOUT if a bounded wait of any kernel on this device (any
- * stream) ran out since the word was last cleared, or PRSINK_ERR_PAGE if a paged call met a
- * length or page index out of range (a timeout is reported first), or PRSINK_ERR_LAUNCH.  Only `stream` is
- * synchronised: kernels still running on other streams may report later. */
+/* Synchronise `stream`, then read the status word of the current device: PRSINK_OK, or
+ * PRSINK_ERR_TIMEOUT if a bounded wait of any kernel on this device (any stream) ran out since that
+ * was last reported, or PRSINK_ERR_PAGE if a paged call met a length or page index out of range, or
+ * PRSINK_ERR_LAUNCH.  The kind reported is cleared; where both were recorded, the timeout comes first
+ * and the next call reports the other.  Only `stream` is synchronised: kernels still running on other
+ * streams may report later. */
 int prsink_sync_status(void* stream);
 
 /* Text of the last host-side error of this thread ("" if none).  Owned by the library. */

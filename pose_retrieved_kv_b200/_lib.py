@@ -429,8 +429,8 @@ def prsink_bank_update_policy(layout: Optional[Layout], policy: BankPolicy, bank
 
 
 def prsink_sync_status(stream=None) -> int:
-    """Synchronise and return the status code (0, PRSINK_ERR_TIMEOUT or PRSINK_ERR_PAGE); does
-    not raise."""
+    """Synchronise and return the status code (0, PRSINK_ERR_TIMEOUT or PRSINK_ERR_PAGE; one kind of
+    error per call, the timeout first); does not raise."""
     return _lib.prsink_sync_status(_stream(stream))
 
 

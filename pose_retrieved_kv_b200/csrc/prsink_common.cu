@@ -163,6 +163,9 @@ int geometry(const prsink_layout* L, Geometry* g) {
   return PRSINK_OK;
 }
 
+// Clears one kind of error and leaves the others, those recorded since the word was read included.
+__global__ void take_status_kernel(int* status, int kind) { atomicAnd(status, ~kind); }
+
 // A block that waits on a barrier nothing signals, until the deadline passes.
 __global__ void wait_timeout_kernel(uint64_t timeout_ns, int* status) {
   __shared__ __align__(8) uint64_t bar;
@@ -215,23 +218,23 @@ int prsink_sync_status(void* stream) {
     set_error("prsink_sync_status: %s", cudaGetErrorString(e));
     return PRSINK_ERR_LAUNCH;
   }
-  if (host) {
-    e = cudaMemsetAsync(sw, 0, sizeof(int), st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) {
-      set_error("prsink_sync_status: %s", cudaGetErrorString(e));
-      return PRSINK_ERR_LAUNCH;
-    }
-    if (host & kStatusTimeout) {
-      set_error("a bounded device wait ran out");
-      return PRSINK_ERR_TIMEOUT;
-    }
-    if (host & kStatusPage) {
-      set_error("a paged call met a sequence length or page index out of range");
-      return PRSINK_ERR_PAGE;
-    }
+  if (!host) return PRSINK_OK;
+  const int kind = host & kStatusTimeout ? kStatusTimeout : kStatusPage;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = cfg.blockDim = dim3(1);
+  cfg.stream = st;
+  e = cudaLaunchKernelEx(&cfg, take_status_kernel, sw, kind);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) {
+    set_error("prsink_sync_status: %s", cudaGetErrorString(e));
+    return PRSINK_ERR_LAUNCH;
   }
-  return PRSINK_OK;
+  if (kind == kStatusTimeout) {
+    set_error("a bounded device wait ran out");
+    return PRSINK_ERR_TIMEOUT;
+  }
+  set_error("a paged call met a sequence length or page index out of range");
+  return PRSINK_ERR_PAGE;
 }
 
 int prsink_debug_wait_timeout(long long timeout_ns, void* stream) {

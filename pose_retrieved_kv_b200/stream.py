@@ -183,8 +183,9 @@ class PRSinkStream:
 
     @staticmethod
     def check_status(stream=None):
-        """Synchronise ``stream`` and raise ``PRSinkError`` if a bounded device wait ran out
-        (on any stream of this device) since the status word was last read."""
+        """Synchronise ``stream`` and raise ``PRSinkError`` if a bounded device wait ran out, or a
+        paged call refused a page or length (on any stream of this device), and has not been
+        reported yet."""
         rc = L.prsink_sync_status(stream)
         if rc != L.PRSINK_OK:
             raise L.PRSinkError(rc, "PRSinkStream", L.prsink_last_error())

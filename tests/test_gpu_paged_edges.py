@@ -37,3 +37,18 @@ def test_scores_of_minus_infinity_weigh_nothing(d, n, length, dead, max_pages):
     assert torch.isfinite(lse[-1, 3:]).all()
     check_attention(dict(pg, n_seqs=n - 1), out[:-1], lse[:-1], q[:-1], k, v, table[:-1],
                     lens[:-1])
+
+
+def test_a_timeout_does_not_hide_a_bad_page():
+    """Both kinds recorded before the status is read: each is reported once, the timeout first."""
+    need_gpu()
+    pg = make(n_seqs=1, n_pages=12, max_pages=4)
+    gen = torch.Generator().manual_seed(55)
+    k, v = (x.cuda() for x in pools(pg, gen))
+    q = torch.randn((1, 4, 64), generator=gen).bfloat16().cuda()
+    table = torch.tensor([[3, 99, -1, 5]], dtype=torch.int32).cuda()
+    attend(pg, q, k, v, table, torch.tensor([64], dtype=torch.int32).cuda())
+    P.prsink_debug_wait_timeout(1000)
+    assert P.prsink_sync_status() == P.PRSINK_ERR_TIMEOUT
+    assert P.prsink_sync_status() == P.PRSINK_ERR_PAGE
+    assert P.prsink_sync_status() == P.PRSINK_OK
