@@ -615,7 +615,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
   const Share sh = find_share<kAttThreads>(p, cta, scan_s, &start_s);
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
-  const uint64_t deadline = globaltimer() + p.timeout_ns;
+  // (a CTA's share of the call may take any time, so each wait has a limit of its own)
+  auto wait = [&](int i, uint32_t parity) {
+    return mbar_wait_limit(bar(i), parity, &ab, p.timeout_ns, p.c.status);
+  };
   const long long u1 = sh.begin(cta + 1);
   Walk w(p, start_s, u1 - sh.begin(cta));
 
@@ -656,8 +659,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       fetch(0, n_page, n_row, n_need);
       if (keys) {
         if (seg >= 2)
-          ok = mbar_wait(bar(B_QFREE + (seg & 1)), ((seg >> 1) - 1) & 1, &ab, deadline,
-                         p.c.status);
+          ok = wait(B_QFREE + (seg & 1), ((seg >> 1) - 1) & 1);
         if (!__all_sync(~0u, ok)) { ok = false; break; }
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(B_QFULL + (seg & 1)), N * D * 2);
@@ -682,7 +684,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
         const bool bad = t_need && (t_page < 0 || t_page >= p.c.n_pages);
         const int np = __popc(__ballot_sync(~0u, t_need));
         const uint32_t bad_mask = __ballot_sync(~0u, bad);
-        if (j >= stages) ok = mbar_wait(bar(b_done + st), parity, &ab, deadline, p.c.status);
+        if (j >= stages) ok = wait(b_done + st, parity);
         if (!__all_sync(~0u, ok)) { ok = false; break; }
         if (lane == 0) {
           if (keys) {
@@ -719,13 +721,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       bool ok = true;
       const uint32_t panel = static_cast<uint32_t>(p.panel_bytes) >> 4;    // descriptor units
       for (; ok && w.left > 0; w.next(p), ++seg) {
-        ok = mbar_wait(bar(B_QFULL + (seg & 1)), (seg >> 1) & 1, &ab, deadline, p.c.status);
+        ok = wait(B_QFULL + (seg & 1), (seg >> 1) & 1);
         const uint64_t b = sdesc_sw128(sb + SM::kQ + (seg & 1) * N * D * 2, 16, 1024);
         for (int i = 0; ok && i < w.n; ++i, ++j, rk.next()) {
           const int st = rk.st, sbuf = j & 1;
-          ok = (j < 2 || mbar_wait(bar(B_SFREE + sbuf), ((j >> 1) - 1) & 1, &ab, deadline,
-                                   p.c.status)) &&
-               mbar_wait(bar(B_KFULL + st), rk.parity, &ab, deadline, p.c.status);
+          ok = (j < 2 || wait(B_SFREE + sbuf, ((j >> 1) - 1) & 1)) &&
+               wait(B_KFULL + st, rk.parity);
           if (!ok) break;
           tc_fence_after();
           const uint64_t a = sdesc_sw128(sb + SM::kK + st * SM::kTileBytes, 16, p.group_bytes);
@@ -749,8 +750,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       for (; ok && w.left > 0; w.next(p)) {
         for (int i = 0; i < w.n; ++i, ++j, rv.next()) {
           const int st = rv.st;
-          ok = mbar_wait(bar(B_VFULL + st), rv.parity, &ab, deadline, p.c.status) &&
-               mbar_wait(bar(B_PFULL + (j & 1)), (j >> 1) & 1, &ab, deadline, p.c.status);
+          ok = wait(B_VFULL + st, rv.parity) &&
+               wait(B_PFULL + (j & 1), (j >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint64_t a = sdesc_sw128(sb + SM::kV + st * SM::kTileBytes, p.panel_bytes,
@@ -790,7 +791,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
     Ring<SM::kVS> rv, rv1, rv2;                    // V stages of tiles j, j - 1, j - 2
     bool ok = true;
     auto o_done = [&](const Ring<SM::kVS>& r) {    // the O product of the tile is complete
-      return mbar_wait(bar(B_ODONE + r.st), r.parity, &ab, deadline, p.c.status);
+      return wait(B_ODONE + r.st, r.parity);
     };
     for (; ok && w.left > 0; w.next(p)) {
       const int kvh = p.by_chunks(w.hc), chunk = w.hc - kvh * p.chunks;
@@ -802,7 +803,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
       for (int i = 0; i < w.n; ++i, ++j, tile.next(p, w.row)) {
         const bool whole = w.row.whole(tile.start, tile.cnt);
         bool live = t < tile.cnt && (whole || w.row.attended(tile.start + t));
-        ok = ok && mbar_wait(bar(B_SDONE + rk.st), rk.parity, &ab, deadline, p.c.status);
+        ok = ok && wait(B_SDONE + rk.st, rk.parity);
         rk.next();
         __syncwarp();
         tc_fence_after();
@@ -913,7 +914,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         if (!whole) {
           // rows without an attended token may hold anything
-          ok = ok && mbar_wait(bar(B_VFULL + rv.st), rv.parity, &ab, deadline, p.c.status);
+          ok = ok && wait(B_VFULL + rv.st, rv.parity);
           if (!live && t < tile.cnt)
             for (int c = 0; c < D / 8; ++c)
               *reinterpret_cast<uint4*>(gb + SM::kV + rv.st * SM::kTileBytes +

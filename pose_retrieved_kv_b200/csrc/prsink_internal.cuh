@@ -134,6 +134,28 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, AbortSt
   return true;
 }
 
+// The same with a limit in ns for this wait alone (its clock starts with the first 1024 tries), for
+// CTAs whose share of a call has no bound: there the waits are short, not their sum.
+__device__ __forceinline__ bool mbar_wait_limit(uint32_t bar, uint32_t parity, AbortState* ab,
+                                                uint64_t limit_ns, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint32_t spins = 0;
+  uint64_t deadline = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++spins & 1023u) == 0) {
+      if (ab->flag) return false;
+      const uint64_t now = globaltimer();
+      if (deadline == 0) deadline = now + limit_ns;
+      if (now > deadline) {
+        ab->flag = 1;
+        atomicOr(status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 // bar.sync on named barrier `id` (1..15) for `count` threads (a multiple of 32): a barrier for
 // a subset of the CTA's warps
 __device__ __forceinline__ void named_bar_sync(int id, int count) {

@@ -52,3 +52,28 @@ def test_a_timeout_does_not_hide_a_bad_page():
     assert P.prsink_sync_status() == P.PRSINK_ERR_TIMEOUT
     assert P.prsink_sync_status() == P.PRSINK_ERR_PAGE
     assert P.prsink_sync_status() == P.PRSINK_OK
+
+
+def test_a_call_may_take_longer_than_a_wait():
+    """A call of about 3 s (600 sequences of 2^20 tokens that share one page, 128 heads), longer
+    than the limit of a wait: every wait in it is short.  A page repeated r = 2^13 times attends as
+    the page itself, its lse log r larger.
+
+    Beside the roundings of a short row: a key's float32 sum takes r additions of 2^-24 each (2^-11),
+    an element of the product 8 r of at most 2^-23 (2^-7 of the average of |v|)."""
+    need_gpu()
+    n, heads, rep = 600, 128, 1 << 13
+    pg = make(n_seqs=n, n_heads=heads, n_kv_heads=heads, page_size=128, n_pages=1, max_pages=rep)
+    gen = torch.Generator().manual_seed(56)
+    k, v = pools(pg, gen)
+    q = torch.randn((n, heads, 64), generator=gen).bfloat16()
+    table = torch.zeros((n, rep), dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), 128 * rep, dtype=torch.int32, device="cuda")
+    out, lse = attend(pg, q.cuda(), k.cuda(), v.cuda(), table, lens)
+    assert P.prsink_sync_status() == P.PRSINK_OK
+    some = [0, 1, 299, 598, 599]
+    once = dict(pg, n_seqs=len(some), max_pages=1)
+    ref, rl, avg = oracle.paged_attention(once, f64(q[some]), f64(k), f64(v), [[0]] * 5, [128] * 5)
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -11 + 2.0 ** -7) * avg
+    assert np.all(np.abs(f64(out[some]) - ref) <= tol)
+    assert np.all(np.abs(f64(lse[some]) - rl - np.log(rep)) <= 2.0 ** -11 + 2.0 ** -11)
