@@ -179,10 +179,17 @@ def _check(rc: int, fn: str):
         raise PRSinkError(rc, fn, _lib.prsink_last_error().decode(errors="replace"))
 
 
+# The handle of a device's current stream without building a Stream object, which takes longer than
+# the rest of a short call's checks.  Private to torch: where it is missing, the public way is taken.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
-        # (the raw handle of torch.cuda.current_stream(), without building a Stream object)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        device = torch.cuda.current_device()         # (initialises CUDA where nothing has yet)
+        if _raw_stream is None:
+            return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -471,7 +478,7 @@ def _dptr(t, name: str, dtype, numel, device: int) -> int:
 
 def _device() -> int:
     """The current device's index (0 before CUDA is in use: no tensor is on a device then)."""
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
 
 
 def prsink_attention_backward_scratch_bytes(layout: Layout) -> int:
