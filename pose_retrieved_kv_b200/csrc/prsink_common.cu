@@ -106,7 +106,10 @@ int make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_
 
 void rope_frequencies(double base, int dims, double* out) {
   // powers of the ratio of neighbours, eight at a time: one exp2 per eight pairs and for the
-  // seven in between (each result is off by two roundings of f64 at most)
+  // seven in between.  The exponent carries log2's ulp, the quotient, and two products: 5 x 2^-53 of
+  // itself, which exp2 turns into 5 |ln base| x 2^-53 of the result; two exp2 (an ulp each), the
+  // constant and two products add 7 x 2^-53.  At base 10^4 together below 2^-47: 7.1e-15 of a
+  // position's angle.
   const double step = -2.0 / dims * std::log2(base);
   double fine[8];
   for (int k = 0; k < 8; ++k) fine[k] = std::exp2(step * k);
