@@ -360,7 +360,7 @@ int prsink_bank_update_policy(const prsink_layout* layout, const prsink_bank_pol
  *   out        bf16 [L_blk][H][d]  the forward's output
  *   lse        f32  [H][L_blk]     the forward's lse (required)
  *   d_out      bf16 [L_blk][H][d]  gradient of the output
- *   dq         bf16 [L_blk][H][d]  written (dq, dk and dv are buffers of their own)
+ *   dq         bf16 [L_blk][H][d]  written (dq, dk, dv and scratch are buffers of their own)
  *   dk, dv     bf16 [H][T][d]      the rows of the slots in `grad_mask` are written, no other
  *              byte; rows of slots without data (valid_mask, dyn_src) get zeros.  Both may be
  *              NULL when grad_mask selects no slot (gradient of the queries alone).
@@ -425,6 +425,8 @@ typedef struct prsink_paged {
  * Rows from cu_new[n_seqs] on are ignored, their q_rot left as it was.  V is copied bit for bit,
  * K and q are rotated in f32 by angles reduced in f64 and rounded once (copied when rope_mode is
  * 0).  No other byte of the pages is written.  Strides are multiples of 8.
+ * The pages and q_rot overlap neither each other nor an input, else the call is refused; q_rot = q
+ * aside, and new rows may lie in pages that get no token.
  * Errors: PRSINK_ERR_ARG, PRSINK_ERR_ALIGN, PRSINK_ERR_UNSUPPORTED, PRSINK_ERR_LAUNCH; on the
  * device PRSINK_ERR_PAGE (a token with no page or outside [0, max_pages*page_size)). */
 int prsink_paged_append(const prsink_paged* paged, const void* k_new, const void* v_new,
@@ -448,6 +450,8 @@ int prsink_paged_append(const prsink_paged* paged, const void* k_new, const void
  *   lse      f32  [n_seqs][n_heads]      natural log-sum-exp (-inf likewise), or NULL
  *   scratch  device memory of prsink_paged_attention_scratch_bytes(paged) bytes, 256-byte
  *            aligned, owned by the caller, not shared with a concurrent call
+ * out, lse and scratch are buffers of their own: overlapping an input (out in the place of q) or each
+ * other is refused.
  * Errors: as prsink_paged_append. */
 int prsink_paged_attention(const prsink_paged* paged, const void* q, const void* k_pages,
                            const void* v_pages, const int* page_table, const int* seq_lens,

@@ -941,12 +941,6 @@ extern "C" int prsink_attention_backward(const prsink_layout* layout, const void
       set_error("%s: null pointer", what);
       return PRSINK_ERR_ARG;
     }
-  for (int i = 5; i < n_bufs; ++i)         // a gradient in the place of an input or of another
-    for (int j = 0; j < i; ++j)
-      if (bufs[i] == bufs[j]) {
-        set_error("%s: dq, dk and dv must be buffers of their own", what);
-        return PRSINK_ERR_ARG;
-      }
   const int D = layout->head_dim;
   if (D != 64 && D != 128) {
     set_error("%s: head_dim %d not supported (64 or 128)", what, D);
@@ -974,6 +968,17 @@ extern "C" int prsink_attention_backward(const prsink_layout* layout, const void
               scratch_bytes);
     return PRSINK_ERR_ARG;
   }
+  const long long row = 2ll * layout->n_heads * D, nq = row * g.L_blk, nk = row * g.T;
+  const Span span[] = {{q, nq}, {k_cache, nk}, {v_cache, nk}, {out, nq},
+                       {lse, 4ll * layout->n_heads * g.L_blk}, {d_out, nq}, {dyn_src, 8},
+                       {dq, nq}, {scratch, static_cast<long long>(pl.total)},
+                       {grad_mask ? dk : nullptr, nk}, {grad_mask ? dv : nullptr, nk}};
+  for (int i = 7; i < 11; ++i)             // in the place of an input or of one another
+    for (int j = 0; j < i; ++j)
+      if (overlap(span[i], span[j])) {
+        set_error("%s: dq, dk, dv and scratch must be buffers of their own", what);
+        return PRSINK_ERR_ARG;
+      }
   Params p{};
   fill(layout, g, p);
   p.grad_mask = grad_mask;

@@ -1275,6 +1275,19 @@ extern "C" int prsink_paged_append(const prsink_paged* paged, const void* k_new,
               "long (in place, q is contiguous)", what, k_stride, v_stride, q_stride);
     return PRSINK_ERR_ARG;
   }
+  const long long pool = 2ll * paged->n_pages * paged->n_kv_heads * paged->page_size * D;
+  const Span table{page_table, 4ll * paged->n_seqs * paged->max_pages};
+  const Span lens{seq_lens, 4ll * paged->n_seqs}, cu{cu_new, 4ll * (paged->n_seqs + 1)};
+  const Span kp{k_pages, pool}, vp{v_pages, pool}, rot{q_rot, 2 * q_row * n_tokens};
+  // (new rows may lie in the pages themselves: a row that is written must not be one that is read)
+  if (overlap_any(kp, {vp, table, lens, cu}) || overlap_any(vp, {table, lens, cu}) ||
+      overlap_any(rot, {kp, vp, table, lens, cu, {k_new, 2 * kv_row, n_tokens, 2 * k_stride},
+                        {v_new, 2 * kv_row, n_tokens, 2 * v_stride}}) ||
+      (q != q_rot && overlap(rot, {q, 2 * q_row, n_tokens, 2 * q_stride}))) {
+    set_error("%s: k_pages, v_pages and q_rot must be buffers of their own (q_rot may be q itself)",
+              what);
+    return PRSINK_ERR_ARG;
+  }
   p.c.table = page_table;
   p.c.lens = seq_lens;
   p.c.status = status_word_ptr();
@@ -1342,6 +1355,19 @@ extern "C" int prsink_paged_attention(const prsink_paged* paged, const void* q,
       scratch_bytes < static_cast<long long>(pl.total)) {
     set_error("%s: scratch must be 256-byte aligned and hold %zu bytes (got %lld)", what, pl.total,
               scratch_bytes);
+    return PRSINK_ERR_ARG;
+  }
+  // CTAs that share a row read its queries and write its results at different times
+  const long long pool = 2ll * p.c.n_pages * p.c.Hkv * p.c.page_size * D;
+  const long long heads = static_cast<long long>(p.c.n_seqs) * p.c.H;
+  const Span in[] = {{q, 2 * heads * D}, {k_pages, pool}, {v_pages, pool},
+                     {page_table, 4ll * p.c.n_seqs * p.c.max_pages}, {seq_lens, 4ll * p.c.n_seqs}};
+  const Span o{out, 2 * heads * D}, l{lse, 4 * heads};
+  const Span sc{scratch, static_cast<long long>(pl.total)};
+  bool own = !overlap_any(o, {l, sc}) && !overlap(l, sc);
+  for (const Span& x : in) own = own && !overlap(o, x) && !overlap(l, x) && !overlap(sc, x);
+  if (!own) {
+    set_error("%s: out, lse and scratch must be buffers of their own", what);
     return PRSINK_ERR_ARG;
   }
   p.c.table = page_table;

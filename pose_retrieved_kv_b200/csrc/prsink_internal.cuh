@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <initializer_list>
+
 #include "../../include/prsink.h"
 
 namespace prsink {
@@ -48,6 +50,26 @@ inline void launch_dependent(void (*kernel)(KArgs...), dim3 grid, int threads, i
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A buffer as a call is given it: `rows` rows of `bytes`, `pitch` bytes apart (one row: contiguous).
+struct Span {
+  const void* at;
+  long long bytes, rows = 1, pitch = 0;
+};
+// Whether any byte of contiguous `a` is one of `b`'s (NULL overlaps nothing).
+inline bool overlap(const Span& a, const Span& b) {
+  if (!a.at || !b.at) return false;
+  const long long d = static_cast<const char*>(a.at) - static_cast<const char*>(b.at);
+  if (b.rows <= 1) return d < b.bytes && d + a.bytes > 0;
+  // the first row of b that does not end before a begins
+  const long long i = d < b.bytes ? 0 : (d - b.bytes) / b.pitch + 1;
+  return i < b.rows && d + a.bytes > i * b.pitch;
+}
+inline bool overlap_any(const Span& a, std::initializer_list<Span> others) {
+  for (const Span& b : others)
+    if (overlap(a, b)) return true;
+  return false;
+}
 
 // 3-D bf16 TMA tensor map (dims d0 x d1 x d2, strides in bytes for dims 1 and 2) with a
 // 64 x box1 x box2 box, 128-byte swizzle, zero fill out of bounds.  PRSINK_OK or ERR_LAUNCH.
