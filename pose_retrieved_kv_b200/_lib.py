@@ -184,9 +184,11 @@ def _check(rc: int, fn: str):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device=None) -> int:
+    """Handle of ``stream``; None: the current stream of ``device`` (None: the current device)."""
     if stream is None:
-        device = torch.cuda.current_device()         # (initialises CUDA where nothing has yet)
+        if device is None:
+            device = torch.cuda.current_device()     # (initialises CUDA where nothing has yet)
         if _raw_stream is None:
             return torch.cuda.current_stream(device).cuda_stream
         return _raw_stream(device)
@@ -504,7 +506,7 @@ def prsink_attention_backward(layout: Layout, q, k_cache, v_cache, out, lse, d_o
         _dptr(dq, "dq", bf, nq, dev), _dptr(dk, "dk", bf, nk, dev), _dptr(dv, "dv", bf, nk, dev),
         int(grad_mask) & 0xFFFFFFFF, _dptr(dyn_src, "dyn_src", torch.int64, 1, dev),
         _dptr(scratch, "scratch", torch.uint8, None, dev),
-        0 if scratch is None else scratch.numel(), _stream(stream))
+        0 if scratch is None else scratch.numel(), _stream(stream, dev))
     _check(rc, "prsink_attention_backward")
 
 
@@ -555,7 +557,7 @@ def prsink_paged_append(paged: Paged, k_new, v_new, k_pages, v_pages, page_table
     cu = 0 if cu_new is None else _dptr(cu_new, "cu_new", _int32, paged.n_seqs + 1, dev)
     qr = 0 if q_rot is None else _dptr(q_rot, "q_rot", _bf16, n * h * d, dev)
     rc = _lib.prsink_paged_append(ctypes.byref(paged), kp, vp, ks, vs, k, v, table, lens, n, cu, qp,
-                                  qs, qr, _stream(stream))
+                                  qs, qr, _stream(stream, dev))
     if rc:
         _check(rc, "prsink_paged_append")
 
@@ -578,5 +580,5 @@ def prsink_paged_attention(paged: Paged, q, k_pages, v_pages, page_table, seq_le
         *_paged_ptrs(paged, k_pages, v_pages, page_table, seq_lens, dev),
         _dptr(out, "out", torch.bfloat16, nd, dev), _dptr(lse, "lse", torch.float32, n, dev),
         _dptr(scratch, "scratch", torch.uint8, None, dev),
-        0 if scratch is None else scratch.numel(), _stream(stream))
+        0 if scratch is None else scratch.numel(), _stream(stream, dev))
     _check(rc, "prsink_paged_attention")
