@@ -6,6 +6,7 @@
 // with q~, k~ the rotated queries and keys and R^T the inverse rotation of the row's position.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "prsink_internal.cuh"
@@ -888,7 +889,7 @@ static int launch(Params& p, cudaStream_t st) {
   // the table of cos / sin as rows of 4 D bytes
   if (!rc) rc = make_map(&mt, p.tab, 2 * D, p.T, 1, 2 * row, 2 * row * p.T, BM, 1);
   if (rc) return rc;
-  static bool allowed[64] = {false};
+  static std::atomic<bool> allowed[64];      // (host threads may call at once)
   int n_sm = 148, dev = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);

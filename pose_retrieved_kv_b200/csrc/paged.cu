@@ -2,6 +2,7 @@
 // the attention of one new token per sequence over the pages.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -1216,7 +1217,7 @@ template <int D, int N>
 static int launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                             const AttParams& p, int grid, cudaStream_t st) {
   const int smem = Smem<D, N>::kBytes + 1024;
-  static bool allowed[64] = {false};
+  static std::atomic<bool> allowed[64];      // (host threads may call at once)
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !allowed[dev]) {
