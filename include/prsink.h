@@ -390,10 +390,11 @@ long long prsink_attention_backward_scratch_bytes(const prsink_layout* layout);
  * rotated once, when it is appended.  Tables and lengths stay on the device (a captured graph
  * can be replayed while they change).  Pages may be shared by sequences (read only).
  *
- * Lengths and page indices are checked on the device: a length is clamped to
- * [0, max_pages*page_size], a page index outside [0, n_pages) that a call has to use makes that
- * page's tokens absent (not written, not attended), and PRSINK_ERR_PAGE is recorded for
- * prsink_sync_status().  No access leaves the buffers. */
+ * Lengths and page indices are checked on the device: the attention clamps a length to
+ * [0, max_pages*page_size], the append leaves out all new tokens of a sequence whose length lies
+ * outside, a page index outside [0, n_pages) that a call has to use makes that page's tokens absent
+ * (not written, not attended), and PRSINK_ERR_PAGE is recorded for prsink_sync_status().  No access
+ * leaves the buffers. */
 typedef struct prsink_paged {
   int n_seqs;            /* rows of page_table; 0 = nothing to do                           */
   int n_heads;           /* query heads, a multiple of n_kv_heads                           */
@@ -443,7 +444,8 @@ int prsink_paged_append(const prsink_paged* paged, const void* k_new, const void
  * read and their table entries not looked at (evicted pages may hold any index).
  * The work is divided evenly over the SMs along the tokens of all sequences and heads; where a
  * (sequence, head) is shared by several CTAs, a second kernel joins their partial results in a
- * fixed order (the same inputs give the same bits on the same device).
+ * fixed order (the same inputs give the same bits on the same device).  The probabilities are
+ * rounded to bf16 as tensor-core operands beside V; scores, sums and lse are f32.
  *   q        bf16 [n_seqs][n_heads][d]   rotated queries (prsink_paged_append)
  *   out      bf16 [n_seqs][n_heads][d]   written; 0 for a sequence with nothing to attend, or with
  *            scores of -inf alone (a score of -inf, from keys with infinities, weighs nothing)

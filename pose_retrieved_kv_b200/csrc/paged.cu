@@ -221,7 +221,8 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
 }
 
 // --------------------------------------------------------------------------------- attention
-// One new token per sequence: HBM-bound, every K and V byte is read once.  The tensor core takes
+// One new token per sequence: HBM-bound, every K and V byte is read once for 64 query heads of its
+// key head (more heads are taken 64 at a time, each with a pass of its own).  The tensor core takes
 // the products with the KEYS as the 128 rows of its tile and the query heads that share a key
 // head as its N columns, so K and V go from TMA straight to the MMA and no thread touches them:
 //   S^T [128 keys][N heads] = K Q^T        (A = K tile, K-major;  B = Q, N rows)
@@ -232,26 +233,41 @@ paged_append_kernel(const __grid_constant__ AppendParams p) {
 // until the row ends.  A tile that exceeds it (and the first one of a row) takes the maximum
 // across the threads, and O and the sums are rescaled.
 //
+// P is rounded to bf16: both operands of an MMA have one type, and V's is bf16.  A probability is
+// off by 2^-8 of itself at most, independently of the others; the sums and lse take it unrounded.
+// The output's error in the 2-norm is 2.1-2.4e-3, of which 1.7e-3 is its own rounding.  A second
+// product with what the rounding leaves would remove the rest, for twice the stores of the softmax
+// (which with 32 and more heads is what bounds the kernel, see below).
+//
 // Work is cut into units of one key tile of one (sequence, key head) row, in row order; every
 // CTA (one per SM) takes an equal, contiguous share, so ragged lengths balance and one long
 // sequence spreads over the device.  A row shared by several CTAs leaves one partial result
 // (O, m, l) each in scratch; a second kernel, launched early and waiting for the first, joins
 // them in CTA order (no counters to clear, no order that depends on timing).
 //
-// Where no row can be longer than kWholeRow tiles, a row belongs to the CTA that holds its first
-// unit and nothing is left to join: a tile more costs less than the second kernel (about 2 us on
-// the device and 2 us on the host).
+// Where the table (or the sinks and the window) leaves no room for a row longer than kWholeRow tiles,
+// a row belongs to the CTA that holds its first unit and nothing is left to join: a tile more costs
+// less than the second kernel.  The lengths themselves are on the device, so a short sequence in a
+// wide table takes both kernels: 256 tokens, one head, 6.6 us on the device with a table of 256 tokens,
+// 8.2 with one of 1024 or 65536; about 2 us more on the host.
 //
 // A tile holds whole pages up to 128 tokens, or up to 128 tokens of one page; one TMA box per
 // page.  Warps: 0-3 softmax, 4 and 7 send K and V, 5 issues the S products, 6 the O products (one
 // thread issues an MMA in about 45 cycles whatever its size, one warp a box in about 100: with one
 // sending warp, pages of 8 took 402 us where two take 319, 64 sequences x 8000 tokens).
 //
-// Measured on a B200 (6551 GB/s copy): 64 sequences x 8000 tokens x 8 key heads of 128, 64 query
-// heads, 316 us (6.6 TB/s) at pages of 16 and more; 48 ragged sequences of up to 16001 tokens,
-// 40 heads on 8, pages of 16, 239 us (6.6 TB/s); one sequence of 14400 tokens, 40 heads, 52.5 us
-// (5.6 TB/s: the start, about 5 us to the first landed tile, and the join are 7 us of it).  A tile
-// takes the softmax warps about 0.5 us where HBM needs 1.45 (head_dim 128) or 0.73 (64).
+// Measured on a B200 (6551 GB/s copy), the same inputs each time: 64 sequences x 8000 tokens x 8 key
+// heads of 128, 64 query heads, 316 us (6.6 TB/s) at pages of 16 and more; 48 ragged sequences of up
+// to 16001 tokens, 40 heads on 8, pages of 16, 239 us (6.6 TB/s; 242-249 with inputs that change);
+// one sequence of 14400 tokens, 40 heads, 52.5 us (5.6 TB/s: the start, about 5 us to the first
+// landed tile, and the join are 7 us of it; 53-54 with inputs that change).
+//
+// Heads on a key head, one key head, 16000 tokens, pages of 16 (64 sequences of width 128 / 128 of 64):
+//   1         98 us (5.4 TB/s) / 115 us (4.6)        33   117 us (4.5) / 180 us (2.9)
+//   16, 17   102, 105 (5.2, 5.0) / 123, 137          64   150 us (3.5) / 234 us (2.2)
+//   32       109 us (4.8) / 155 us (3.4)            128   244 us: two passes / 426 us
+// A tile takes the softmax warps about 0.5 us at N = 16 where HBM needs 1.45 (width 128) or 0.73 (64),
+// and about four times that at N = 64, where they are the bound (255 registers and 204 bytes spilled).
 constexpr int kTile = 128;                 // key rows of a tile = TMEM lanes
 constexpr int kAttThreads = 256;
 constexpr int kKeyWarp = 4, kScoreWarp = 5, kOutWarp = 6, kValueWarp = 7;
@@ -601,10 +617,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
     tmem_alloc(smem_u32(&tmem_base_s), SM::kTmemCols);
     tmem_relinquish();
   }
-  // columns of P that no head fills must be finite; V rows that no box fills (pages that do not
-  // divide a tile) too: P is 0 there, but 0 * NaN is not
-  for (int i = threadIdx.x; i < 2 * SM::kPBytes / 16; i += kAttThreads)
-    reinterpret_cast<uint4*>(gb + SM::kP)[i] = make_uint4(0, 0, 0, 0);
+  // V rows that no box fills (pages that do not divide a tile) must be finite: P is 0 there, but
+  // 0 * NaN is not.  (Columns of P that no head fills may hold anything: they reach only columns of O
+  // that nobody reads.)
   if (!p.tiles_per_page && p.tile_tokens < kTile)
     for (int i = threadIdx.x; i < SM::kVS * SM::kTileBytes / 16; i += kAttThreads)
       reinterpret_cast<uint4*>(gb + SM::kV)[i] = make_uint4(0, 0, 0, 0);
@@ -1164,7 +1179,7 @@ static int check_ptrs(const char* what, std::initializer_list<const void*> bufs,
 }
 
 // Tokens per CTA and CTAs per token, measured on a B200 (one token per CTA / four):
-//   16384 tokens x 56 rows of 256 B (470 MB)   91.9 us / 81.5 us (5.8 TB/s)
+//   16384 tokens x 56 rows of 256 B (470 MB)   91.9 us / 81.5 us (5.8 TB/s; 84-87 when inputs change)
 //   2700 tokens x 120 rows (166 MB)            29.8 us (5.6 TB/s) / 38.1 us
 //   64 tokens x 56 rows                         3.7 us / 6.8 us; one token split over 4: 3.3 us
 // Short tokens share a CTA (and the latency of looking up their place) while the grid still fills
